@@ -236,6 +236,134 @@ I4_API int i4_embed_gather(const uint16_t *table, const int32_t *tokens, uint16_
 I4_API int i4_argmax_rows(const float *logits, int32_t *tokens, int32_t *pos, int32_t *ctx_len, int B, int N,
                           void *stream);
 
+/* ------------------------------------------------- several new tokens of several sequences
+ *
+ * Calls that take a ragged batch of new tokens share these arguments:
+ *   q_start   [B + 1] int32 device array, not decreasing: rows q_start[b] ..
+ *             q_start[b + 1] - 1 of the call's T rows are the new tokens of
+ *             sequence b (none when both are equal). Rows from q_start[B] on
+ *             belong to nobody and their outputs are left as they were.
+ *   ctx_len   [B] int32 device array: tokens of sequence b INCLUDING the new
+ *             ones, so new token i of n stands at position ctx_len[b] - n + i.
+ *   page_table, page_size, max_pages_per_seq as for paged_gqa_decode;
+ *   num_pages pages in each pool: a page id outside [0, num_pages) among those in
+ *             use is never followed: it reads as zeros, and what would be written there is dropped.
+ * q_start, ctx_len and page_table are read on the device, so a captured call
+ * follows them from replay to replay.
+ */
+
+/*
+ * Table of rotary angles: cs[p][i] = m * (cos, sin)(p * f_i), i < rotary_dim / 2,
+ * in fp32 from 64-bit angles, with f_i = theta^(-2i / rotary_dim) and
+ *   I4_ROPE_NONE    m = 1;
+ *   I4_ROPE_LINEAR  f_i / factor, m = 1;
+ *   I4_ROPE_YARN    f_i (1 - r_i) + (f_i / factor) r_i, r_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *                   lo, hi = floor, ceil of the pairs that turn 32 times and
+ *                   once over original_ctx positions (clamped to [0, rotary_dim - 1]),
+ *                   m = 0.1 ln(factor) + 1.
+ *   cs [max_pos][rotary_dim / 2][2] fp32, 16-byte aligned; rotary_dim a multiple
+ *   of 16 up to 128; theta > 1; factor >= 1. Made once, like weights.
+ */
+#define I4_ROPE_NONE 0
+#define I4_ROPE_LINEAR 1
+#define I4_ROPE_YARN 2
+I4_API int i4_rope_table(float *cs, int max_pos, int rotary_dim, double theta, int scaling, double factor,
+                         int original_ctx, void *stream);
+
+/*
+ * Rotary positions of new tokens, out of place, and the append of their K/V:
+ * the first rotary_dim values of every q and k head of row t are rotated by the
+ * angles cs[position] in pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * `interleaved`; the rest and the v heads pass bit for bit. q goes to
+ * q_out [T][Hq][128], k and v to the position's page slot of the pools.
+ *   qkv [T] rows of [q heads | k heads | v heads], qkv_stride elements apart
+ *   (>= (Hq + 2 Hkv) * 128, a multiple of 8); cs from i4_rope_table with the
+ *   same rotary_dim and max_pos. qkv, cs, q_out and the pools 16-byte aligned; q_out does
+ *   not overlap qkv. D == 128, Hq and Hkv <= 4096.
+ * A token whose position is negative, >= max_pos or behind the table row is
+ * skipped (q_out keeps its row); one whose page id is outside [0, num_pages) writes q_out only.
+ * Two tokens that name the same page slot leave either one's values there.
+ */
+I4_API int i4_rope_append_chunk(const uint16_t *qkv, long long qkv_stride, const int32_t *q_start, const int32_t *ctx_len,
+                                const float *cs, int max_pos, int rotary_dim, int interleaved, int T, int B, int Hq,
+                                int Hkv, int D, uint16_t *q_out, uint16_t *k_pool, uint16_t *v_pool,
+                                const int32_t *page_table, int page_size, int max_pages_per_seq, int num_pages,
+                                void *stream);
+
+/*
+ * Attention of new tokens over the pages, which hold their own K/V already.
+ * The token at position p of sequence b sees the positions t <= p, and only
+ * t > p - window when window > 0; for query head h and kv head g = h / (Hq / Hkv)
+ *   out = sum_t softmax_t(scale * q . K[g][t]) V[g][t]      (fp32 sums, fp16 out)
+ * P = exp(s - m) is rounded to fp16 before it meets V. A token that sees
+ * nothing (a negative position) gives zeros; positions behind the page-table row
+ * are not seen. What lies in a page outside a token's positions, NaN included,
+ * does not reach its output.
+ *   q [T] rows of Hq * 128 fp16, q_stride elements apart (>= Hq * 128, a
+ *   multiple of 8); out [T][Hq][128]; both and the pools 16-byte aligned; out does not overlap q;
+ *   max_q  the longest chunk of the call if the host knows it, else 0: picks a
+ *          variant, never the result's meaning;
+ *   ws     workspace of i4_paged_gqa_chunk_ws_bytes() bytes (the same for every
+ *          shape), 256-byte aligned, with any contents. Calls sharing one ws must not overlap on the GPU.
+ * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 8, page_size a power of two in
+ * [8, 128], scale > 0, T <= 2^20, B <= 65536, max_pages_per_seq * page_size <= 2^20.
+ */
+I4_API size_t i4_paged_gqa_chunk_ws_bytes(void);
+I4_API int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
+                              const int32_t *page_table, const int32_t *q_start, const int32_t *ctx_len, uint16_t *out, int T,
+                              int B, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages, int window,
+                              int max_q, float scale, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Pages of a cache. `pools` is a HOST array of n_pools device pointers, each
+ * [num_pages][Hkv][page_size][D] of 16-bit values, 16-byte aligned (all layers'
+ * K and V pools: one call moves a page in all of them).
+ *
+ * refs[p] counts the sequences that hold page p (0 = free; a caller keeps a page out
+ * of the cache by counting it itself). Sequence s holds page_table[s][0 ..
+ * ceil(ctx_len[s] / page_size)); a page that is not full has one holder. Pages
+ * are handed out lowest id first, in the order of the requests, so the same
+ * calls give the same pages.
+ *
+ *   i4_kv_pages_copy     page src[i] -> dst[i] in every pool; no page may be named as both, and no
+ *                        dst twice; entries outside [0, num_pages) are skipped.
+ *   i4_kv_pages_reserve  room for add[i] more tokens of sequence seqs[i]: new pages
+ *                        into its row, ctx_len += add[i].
+ *   i4_kv_pages_fork     sequence dst[i] becomes a continuation of src[i]: what dst
+ *                        held is given back, src's full pages are shared, and the filled rows of a
+ *                        last page that is not full are copied to a new page.
+ *   i4_kv_pages_free     the sequences' pages are given back, ctx_len = 0, rows -1
+ *                        (ids outside [0, n_seqs) are skipped; naming one twice is harmless).
+ *   i4_kv_pages_compact  moves the n_live pages in use to ids 0 .. n_live - 1: the
+ *                        j-th free id below n_live takes the j-th used page at or above it;
+ *                        refs and page_table follow. n_live (device, or NULL) gets the count.
+ * status [n] (device, or NULL): 0 done; 1 not enough free pages; 2 refused: an id
+ * outside [0, n_seqs), a sequence named by an earlier entry (dst for a fork), a src that
+ * is some entry's dst, a negative add, or more tokens than the row holds. A
+ * refused entry changes nothing, except that a fork that finds no page leaves dst
+ * empty. Of a reserve, the first request that does not fit and every later one
+ * that needs a page get status 1.
+ *   n <= n_seqs <= 16384; num_pages <= 2^20; ws: i4_kv_pages_ws_bytes(num_pages, n_seqs) bytes,
+ *   16-byte aligned, any contents. Calls that share ws or the cache's arrays must not overlap.
+ */
+typedef struct i4_kv_cache {
+    int32_t *page_table; /* [n_seqs][max_pages_per_seq] */
+    int32_t *ctx_len;    /* [n_seqs] */
+    int32_t *refs;       /* [num_pages] */
+    int n_seqs, max_pages_per_seq, page_size, num_pages;
+} i4_kv_cache;
+
+I4_API size_t i4_kv_pages_ws_bytes(int num_pages, int n_seqs);
+I4_API int i4_kv_pages_copy(void *const *pools, int n_pools, int num_pages, int Hkv, int page_size, int D, const int32_t *src,
+                            const int32_t *dst, int n, void *stream);
+I4_API int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs, const int32_t *add, int n, int32_t *status,
+                               void *ws, size_t ws_bytes, void *stream);
+I4_API int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, const int32_t *src,
+                            const int32_t *dst, int n, int32_t *status, void *ws, size_t ws_bytes, void *stream);
+I4_API int i4_kv_pages_free(const i4_kv_cache *cache, const int32_t *seqs, int n, void *stream);
+I4_API int i4_kv_pages_compact(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, int32_t *n_live,
+                               void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- decode step */
 
 typedef struct i4_model_desc {

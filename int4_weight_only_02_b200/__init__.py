@@ -60,6 +60,13 @@ class RmsnormRopeArgs(ctypes.Structure):
                 ("max_pages_per_seq", _i)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("page_table", _vp), ("ctx_len", _vp), ("refs", _vp), ("n_seqs", _i), ("max_pages_per_seq", _i),
+                ("page_size", _i), ("num_pages", _i)]
+
+
+_ll, _d, _pools = ctypes.c_longlong, ctypes.c_double, ctypes.POINTER(_vp)
+
 _SIGS = {
     "i4_last_error": (ctypes.c_char_p, []),
     "i4_version": (ctypes.c_char_p, []),
@@ -80,6 +87,18 @@ _SIGS = {
     "i4_rmsnorm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _f, _vp]),
     "i4_rope_kv_append": (_i, [_vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _i, _vp]),
     "silu_mul": (_i, [_vp, _vp, _i, _i, _vp]),
+    "i4_rope_table": (_i, [_vp, _i, _i, _d, _i, _d, _i, _vp]),
+    "i4_rope_append_chunk": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
+                                  _vp]),
+    "i4_paged_gqa_chunk_ws_bytes": (_sz, []),
+    "i4_paged_gqa_chunk": (_i, [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz,
+                                _vp]),
+    "i4_kv_pages_ws_bytes": (_sz, [_i, _i]),
+    "i4_kv_pages_copy": (_i, [_pools, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]),
+    "i4_kv_pages_reserve": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_fork": (_i, [ctypes.POINTER(KvCacheDesc), _pools, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_free": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _vp]),
+    "i4_kv_pages_compact": (_i, [ctypes.POINTER(KvCacheDesc), _pools, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "decode_step_graph_create": (_i, [ctypes.POINTER(ModelDesc), ctypes.POINTER(ModelWeights),
                                       ctypes.POINTER(SeqState), ctypes.POINTER(_vp)]),
     "decode_step_graph_replay": (_i, [_vp, _vp]),
@@ -299,6 +318,212 @@ def silu_mul(gate_up, out=None, stream=None):
         out = torch.empty((M, I2 // 2), device=gate_up.device, dtype=torch.float16)
     _check(lib().silu_mul(_p(g2), _p(out), M, I2 // 2, _stream(stream)), "silu_mul")
     return out if gate_up.dim() == 2 else out.view(-1)
+
+
+# ------------------------------------------------------------------ several new tokens of several sequences
+
+def _refuse(name: str, what: str):
+    raise I4Error(I4_EINVAL, f"{name}: {what}")
+
+
+def _tensors(name: str, *groups):
+    """Refuses tensors that the call could not follow: every (tensor, dtype, dims) has that type and number of
+    dimensions, is contiguous and lies on the current CUDA device (whose current stream the call uses)."""
+    import torch
+    for t, dtype, dims in groups:
+        if t.dtype is not dtype or t.dim() != dims or not t.is_contiguous():
+            _refuse(name, f"a contiguous {dtype} tensor of {dims} dimensions is needed, got {t.dtype} {tuple(t.shape)}")
+    dev = groups[0][0].device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(name, f"tensors on the current CUDA device are needed, got {dev}")
+    for t, _, _ in groups:
+        if t.device != dev:
+            _refuse(name, f"tensors on {dev} and {t.device}")
+    return dev
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+
+
+def rope_table(max_pos: int, rotary_dim: int = 128, theta: float = 1e6, scaling: str = "none", factor: float = 1.0,
+               original_ctx: int = 0, device="cuda", stream=None):
+    """Angles of positions 0..max_pos-1 for ``rope_append_chunk``: [max_pos][rotary_dim/2][2] fp32 (cos, sin).
+    ``scaling``: "none", "linear" (positions / factor) or "yarn" (frequencies blended over original_ctx)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        _refuse("rope_table", f"scaling {scaling!r} is none of {sorted(ROPE_SCALINGS)}")
+    cs = torch.empty((max(int(max_pos), 0), max(int(rotary_dim), 0) // 2, 2), dtype=torch.float32, device=device)
+    if cs.device.type != "cuda" or cs.device.index != torch.cuda.current_device():
+        _refuse("rope_table", f"the current CUDA device is needed, got {cs.device}")
+    _check(lib().i4_rope_table(_p(cs), int(max_pos), int(rotary_dim), float(theta), ROPE_SCALINGS[scaling],
+                               float(factor), int(original_ctx), _stream(stream)), "rope_table")
+    return cs
+
+
+def rope_append_chunk(qkv, q_start, ctx_len, cs, Hq: int, Hkv: int, k_pool, v_pool, page_table, q_out=None,
+                      interleaved: bool = False, stream=None):
+    """Rotates the q and k heads of new tokens (qkv [T][(Hq+2Hkv)*128], rows may be strided) by the angles ``cs`` of
+    their positions; q goes to q_out [T][Hq][128] (returned; rows behind the last sequence are left alone), k and v to
+    the pages. The rotated part of a head is cs.shape[1] * 2 values."""
+    import torch
+    name = "rope_append_chunk"
+    f16, i32 = torch.float16, torch.int32
+    if qkv.dim() != 2 or qkv.dtype is not f16 or (qkv.stride(1) != 1 and qkv.shape[1] > 1):
+        _refuse(name, "qkv [T][(Hq+2Hkv)*128] fp16 with adjacent columns is needed")
+    T, B = qkv.shape[0], page_table.shape[0]
+    if q_out is None:
+        q_out = torch.zeros((T, Hq, 128), device=qkv.device, dtype=f16)
+    dev = _tensors(name, (q_start, i32, 1), (ctx_len, i32, 1), (cs, torch.float32, 3), (k_pool, f16, 4), (v_pool, f16, 4),
+                   (page_table, i32, 2), (q_out, f16, 3))
+    num_pages, hkv, P, D = k_pool.shape
+    if (qkv.device != dev or qkv.shape[1] != (Hq + 2 * Hkv) * D or hkv != Hkv or v_pool.shape != k_pool.shape
+            or q_out.shape != (T, Hq, D) or q_start.numel() != B + 1 or ctx_len.numel() != B or cs.shape[2] != 2):
+        _refuse(name, f"shapes do not match: qkv {tuple(qkv.shape)}, pools {tuple(k_pool.shape)} {tuple(v_pool.shape)}, "
+                      f"q_out {tuple(q_out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
+    if T == 0 or B == 0:
+        return q_out
+    _check(lib().i4_rope_append_chunk(_p(qkv), qkv.stride(0), _p(q_start), _p(ctx_len), _p(cs), cs.shape[0],
+                                      cs.shape[1] * 2, int(interleaved), T, B, Hq, Hkv, D, _p(q_out), _p(k_pool),
+                                      _p(v_pool), _p(page_table), P, page_table.shape[1], num_pages, _stream(stream)),
+           name)
+    return q_out
+
+
+def paged_gqa_chunk_ws_bytes() -> int:
+    return int(lib().i4_paged_gqa_chunk_ws_bytes())
+
+
+def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, window: int = 0, max_q: int = 0,
+                    scale=None, ws=None, stream=None):
+    """Attention of new tokens (q [T][Hq][128], token rows may be strided) over the pages that hold their own K/V
+    already: row i of sequence b sees the positions up to ctx_len[b] - n + i, the last ``window`` of them if not 0.
+    ``max_q``: the longest chunk if known on the host (a hint). ``ws``: paged_gqa_chunk_ws_bytes() bytes, any contents;
+    allocated when not given. Rows behind the last sequence are left alone (zeros in an ``out`` made here)."""
+    import torch
+    name = "paged_gqa_chunk"
+    f16, i32 = torch.float16, torch.int32
+    if q.dim() != 3 or q.dtype is not f16 or q.stride(2) != 1 or (q.stride(1) != q.shape[2] and q.shape[1] > 1):
+        _refuse(name, "q [T][Hq][128] fp16 with adjacent heads is needed")
+    T, Hq, D = q.shape
+    B = page_table.shape[0]
+    if out is None:
+        out = torch.zeros((T, Hq, D), device=q.device, dtype=f16)
+    dev = _tensors(name, (k_pool, f16, 4), (v_pool, f16, 4), (page_table, i32, 2), (q_start, i32, 1), (ctx_len, i32, 1),
+                   (out, f16, 3))
+    num_pages, Hkv, P, dk = k_pool.shape
+    if (q.device != dev or dk != D or v_pool.shape != k_pool.shape or out.shape != q.shape or q_start.numel() != B + 1
+            or ctx_len.numel() != B):
+        _refuse(name, f"shapes do not match: q {tuple(q.shape)}, pools {tuple(k_pool.shape)} {tuple(v_pool.shape)}, out "
+                      f"{tuple(out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
+    if T == 0 or B == 0:
+        return out
+    if ws is None:
+        ws = torch.empty(paged_gqa_chunk_ws_bytes(), device=dev, dtype=torch.uint8)
+    _check(lib().i4_paged_gqa_chunk(_p(q), q.stride(0) if T > 1 else Hq * D, _p(k_pool), _p(v_pool), _p(page_table),
+                                    _p(q_start), _p(ctx_len), _p(out), T, B, Hq, Hkv, D, P, page_table.shape[1], num_pages,
+                                    int(window), int(max_q), 1.0 / D ** 0.5 if scale is None else float(scale), _p(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)), name)
+    return out
+
+
+def _pool_array(name: str, pools):
+    """(host array of the pools' addresses, shape of a pool) of a sequence of equal fp16 pools."""
+    import torch
+    shape = pools[0].shape if len(pools) else ()
+    if len(shape) != 4:
+        _refuse(name, "pools [num_pages][Hkv][page_size][D] are needed")
+    dev = pools[0].device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(name, f"pools on the current CUDA device are needed, got {dev}")
+    for t in pools:
+        if t.shape != shape or t.element_size() != 2 or not t.is_contiguous() or t.device != dev:
+            _refuse(name, "pools of one shape, two bytes a value, contiguous and on one device are needed")
+    return (_vp * len(pools))(*[t.data_ptr() for t in pools]), shape
+
+
+def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, *lists):
+    import torch
+    i32 = torch.int32
+    _tensors(name, (page_table, i32, 2), (ctx_len, i32, 1), (refs, i32, 1), *[(t, i32, 1) for t in lists])
+    if ctx_len.numel() != page_table.shape[0] or any(t.numel() != lists[0].numel() for t in lists):
+        _refuse(name, f"shapes do not match: page_table {tuple(page_table.shape)}, ctx_len {tuple(ctx_len.shape)}, lists "
+                      f"{[t.numel() for t in lists]}")
+    return KvCacheDesc(page_table.data_ptr(), ctx_len.data_ptr(), refs.data_ptr(), page_table.shape[0],
+                       page_table.shape[1], int(page_size), refs.numel())
+
+
+def kv_pages_ws_bytes(num_pages: int, n_seqs: int) -> int:
+    return int(lib().i4_kv_pages_ws_bytes(num_pages, n_seqs))
+
+
+def _kv_ws(ws, page_table, refs):
+    import torch
+    if ws is None:
+        ws = torch.empty(max(kv_pages_ws_bytes(refs.numel(), page_table.shape[0]), 256), dtype=torch.uint8,
+                         device=refs.device)
+    return ws
+
+
+def kv_pages_copy(pools, src, dst, stream=None):
+    """Page src[i] -> dst[i] in every pool (device int32 lists; no page may be both source and target)."""
+    import torch
+    arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_copy", pools)
+    _tensors("kv_pages_copy", (src, torch.int32, 1), (dst, torch.int32, 1))
+    if src.numel() != dst.numel():
+        _refuse("kv_pages_copy", f"{src.numel()} sources and {dst.numel()} targets")
+    _check(lib().i4_kv_pages_copy(arr, len(pools), num_pages, Hkv, P, D, _p(src), _p(dst), src.numel(), _stream(stream)),
+           "kv_pages_copy")
+
+
+def kv_pages_reserve(page_table, ctx_len, refs, page_size: int, seqs, add, status=None, ws=None, stream=None):
+    """Room for add[i] more tokens of sequence seqs[i]: free pages into its row, ctx_len += add[i]. Returns status [n]
+    (0 done, 1 not enough free pages, 2 refused)."""
+    import torch
+    if status is None:
+        status = torch.empty_like(seqs)
+    desc = _cache_desc("kv_pages_reserve", page_table, ctx_len, refs, page_size, seqs, add, status)
+    ws = _kv_ws(ws, page_table, refs)
+    _check(lib().i4_kv_pages_reserve(ctypes.byref(desc), _p(seqs), _p(add), seqs.numel(), _p(status), _p(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_reserve")
+    return status
+
+
+def kv_pages_fork(pools, page_table, ctx_len, refs, src, dst, status=None, ws=None, stream=None):
+    """Sequence dst[i] becomes a continuation of src[i]: full pages shared, a last page that is not full copied in every
+    pool. Returns status [n] (0 done, 1 no free page and dst left empty, 2 refused)."""
+    import torch
+    arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_fork", pools)
+    if status is None:
+        status = torch.empty_like(src)
+    desc = _cache_desc("kv_pages_fork", page_table, ctx_len, refs, P, src, dst, status)
+    if refs.numel() != num_pages:
+        _refuse("kv_pages_fork", f"{refs.numel()} reference counts for {num_pages} pages")
+    ws = _kv_ws(ws, page_table, refs)
+    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr, len(pools), Hkv, D, _p(src), _p(dst), src.numel(), _p(status),
+                                  _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_fork")
+    return status
+
+
+def kv_pages_free(page_table, ctx_len, refs, page_size: int, seqs, stream=None):
+    """The pages of the sequences are given back; their rows become -1 and their ctx_len 0."""
+    desc = _cache_desc("kv_pages_free", page_table, ctx_len, refs, page_size, seqs)
+    _check(lib().i4_kv_pages_free(ctypes.byref(desc), _p(seqs), seqs.numel(), _stream(stream)), "kv_pages_free")
+
+
+def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, stream=None):
+    """Moves the pages in use to the lowest ids in every pool; page_table and refs follow. Returns n_live [1], the number
+    of pages in use."""
+    import torch
+    arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_compact", pools)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    desc = _cache_desc("kv_pages_compact", page_table, ctx_len, refs, P, n_live)
+    if refs.numel() != num_pages or n_live.numel() != 1:
+        _refuse("kv_pages_compact", f"{refs.numel()} reference counts for {num_pages} pages, n_live of {n_live.numel()}")
+    ws = _kv_ws(ws, page_table, refs)
+    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr, len(pools), Hkv, D, _p(n_live), _p(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_compact")
+    return n_live
 
 
 from .runtime import BatchedDecode, DecodeGraph, DeviceModel, Prefill, Sequence  # noqa: E402,F401

@@ -1,0 +1,539 @@
+// The pages of a cache: copying, reserving, forking, freeing and compacting.
+//
+// State, all on the device:  page_table [S][max_pages], ctx_len [S] (tokens of
+// each sequence) and refs [num_pages] (sequences that hold the page; 0 = free).
+// Sequence s holds the pages page_table[s][0 .. ceil(ctx_len[s] / P)). A page
+// that is not full has one holder, since a fork copies it.
+//
+// Every operation is deterministic: pages are handed out lowest id first, in the
+// order of the requests. Reserving, forking and compacting decide in one CTA (a
+// few thousand integers, bound by the latency of a handful of dependent passes
+// over them: several CTAs would need grid-wide barriers that cost as much) and
+// leave a list of copies in the workspace; a second kernel over the whole GPU
+// moves the data of all pools at once and is bound by HBM.
+#include "common.cuh"
+
+namespace i4 {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxSeqs = 16384;      // a 64 KB table of owners in shared memory
+constexpr int kMaxPages = 1 << 20;   // a sum over 1024 requests of at most this many pages fits 31 bits
+constexpr int kPoolsPerLaunch = 256;  // pool addresses in the kernel's parameters
+
+struct PoolPtrs {
+    unsigned char *p[kPoolsPerLaunch];
+};
+
+// ------------------------------------------------------------------ block-wide scans
+
+struct ScanSmem {
+    int warp[kPlanThreads / 32];
+    int total;
+};
+
+// Exclusive prefix sum of v over the CTA's threads, and the sum over all of them.
+__device__ __forceinline__ int block_scan(int v, int &total, ScanSmem &sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) sm.warp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int w = sm.warp[lane];
+        int iw = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, iw, o);
+            if (lane >= o) iw += u;
+        }
+        sm.warp[lane] = iw - w;
+        if (lane == 31) sm.total = iw;
+    }
+    __syncthreads();
+    const int r = sm.warp[warp] + inc - v;
+    total = sm.total;
+    __syncthreads();  // the scratch is free for the next scan
+    return r;
+}
+
+// The `want` lowest free pages in ascending order to list[]; returns how many there are (at most want).
+__device__ __forceinline__ int find_free(const int32_t *refs, int num_pages, int want, int32_t *list, ScanSmem &sm) {
+    int found = 0;
+    for (int p0 = 0; p0 < num_pages && found < want; p0 += 4 * kPlanThreads) {  // block-uniform trips
+        const int p = p0 + 4 * threadIdx.x;
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = p + i < num_pages ? __ldcg(refs + p + i) : 1;  // written by atomics: past L1
+        int total;
+        int at = found + block_scan((r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0), total, sm);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r[i] == 0) {
+                if (at < want) list[at] = p + i;
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();
+    return found < want ? found : want;
+}
+
+__device__ __forceinline__ int pages_of(int ctx, int P, int max_pages) {
+    const int n = ctx <= 0 ? 0 : (ctx - 1) / P + 1;
+    return n < max_pages ? n : max_pages;
+}
+
+struct CacheArgs {
+    int32_t *table, *ctx_len, *refs;
+    int S, max_pages, P, num_pages;
+};
+
+// ------------------------------------------------------------------ plans (one CTA)
+
+// Workspace of every operation: count | a | b | c, arrays of `cap` int32 each.
+struct Lists {
+    int32_t *count, *a, *b, *c;
+};
+__host__ __device__ inline Lists ws_lists(void *ws, size_t cap) {
+    int32_t *p = reinterpret_cast<int32_t *>(ws);
+    return {p, p + 64, p + 64 + cap, p + 64 + 2 * cap};
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const CacheArgs c, const int32_t *seqs, const int32_t *add,
+                                                                  int n, int32_t *status, Lists ws) {
+    extern __shared__ int owner[];
+    __shared__ ScanSmem sm;
+    const int tid = threadIdx.x;
+    for (int s = tid; s < c.S; s += kPlanThreads) owner[s] = n;
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads)
+        if (seqs[i] >= 0 && seqs[i] < c.S) atomicMin(&owner[seqs[i]], i);
+    __syncthreads();
+    // pages that each request needs, and where its pages begin in the list of free ones
+    int want = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int need = -1;
+        if (i < n) {
+            const int s = seqs[i];
+            if (s >= 0 && s < c.S && owner[s] == i && add[i] >= 0 && c.ctx_len[s] >= 0 &&
+                (long long)c.ctx_len[s] + add[i] <= (long long)c.max_pages * c.P)
+                need = min(pages_of(c.ctx_len[s] + add[i], c.P, c.max_pages) - pages_of(c.ctx_len[s], c.P, c.max_pages),
+                           c.num_pages + 1);
+        }
+        int total;
+        const int at = want + block_scan(need > 0 ? need : 0, total, sm);
+        if (i < n) {
+            ws.b[i] = need;
+            ws.c[i] = at;
+        }
+        want = want > c.num_pages - total ? c.num_pages + 1 : want + total;  // more than exist is never granted
+    }
+    const int have = find_free(c.refs, c.num_pages, want < c.num_pages ? want : c.num_pages, ws.a, sm);
+    for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {  // one warp per request
+        const int need = ws.b[i], at = ws.c[i], lane = tid & 31;
+        int st = 0;
+        if (need < 0)
+            st = 2;
+        else if (need > 0 && at + need > have)
+            st = 1;
+        if (st == 0) {
+            const int s = seqs[i], old = pages_of(c.ctx_len[s], c.P, c.max_pages);
+            for (int j = lane; j < need; j += 32) {
+                const int page = ws.a[at + j];
+                c.table[(size_t)s * c.max_pages + old + j] = page;
+                c.refs[page] = 1;
+            }
+            __syncwarp();
+            if (lane == 0) c.ctx_len[s] += add[i];
+        }
+        if (lane == 0 && status) status[i] = st;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c, const int32_t *src, const int32_t *dst, int n,
+                                                               int32_t *status, Lists ws) {
+    extern __shared__ int owner[];
+    __shared__ ScanSmem sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t kNone = n;
+    for (int s = tid; s < c.S; s += kPlanThreads) owner[s] = kNone;
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads)
+        if (dst[i] >= 0 && dst[i] < c.S) atomicMin(&owner[dst[i]], i);
+    __syncthreads();
+    auto valid = [&](int i) {
+        const int s = src[i], d = dst[i];
+        return s >= 0 && s < c.S && d >= 0 && d < c.S && owner[d] == i && owner[s] == kNone;
+    };
+    // give back what the targets hold, and hold the full pages of the sources
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        if (!valid(i)) continue;
+        const int32_t *old = c.table + (size_t)dst[i] * c.max_pages, *row = c.table + (size_t)src[i] * c.max_pages;
+        const int held = pages_of(c.ctx_len[dst[i]], c.P, c.max_pages);
+        const int full = min(max(c.ctx_len[src[i]], 0) / c.P, c.max_pages);
+        for (int j = lane; j < max(held, full); j += 32) {
+            const int a = j < held ? old[j] : -1, b = j < full ? row[j] : -1;
+            if (a >= 0 && a < c.num_pages) atomicSub(&c.refs[a], 1);
+            if (b >= 0 && b < c.num_pages) atomicAdd(&c.refs[b], 1);
+        }
+    }
+    __syncthreads();
+    // one free page for every source whose last page is not full
+    int want = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int need = 0;
+        if (i < n && valid(i)) {
+            const int ctx = max(c.ctx_len[src[i]], 0);
+            need = ctx % c.P != 0 && ctx / c.P < c.max_pages;
+        }
+        int total;
+        const int at = want + block_scan(need, total, sm);
+        if (i < n) ws.b[i] = need ? at : -1;
+        want += total;
+    }
+    const int have = find_free(c.refs, c.num_pages, want, ws.a, sm);
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        const bool ok = valid(i);
+        const int at = ws.b[i];
+        __syncwarp();  // every lane has read ws.b[i], which the copy list below shares
+        int from = 0, to = 0, fill = 0;
+        const bool room = at < 0 || at < have;
+        if (ok) {
+            const int32_t *row = c.table + (size_t)src[i] * c.max_pages;
+            int32_t *out = c.table + (size_t)dst[i] * c.max_pages;
+            const int ctx = min(max(c.ctx_len[src[i]], 0), c.max_pages * c.P), full = ctx / c.P;
+            if (room) {
+                for (int j = lane; j < c.max_pages; j += 32) out[j] = j < full ? row[j] : -1;
+            } else {  // no page left: the target stays empty and holds nothing
+                for (int j = lane; j < full; j += 32)
+                    if (row[j] >= 0 && row[j] < c.num_pages) atomicSub(&c.refs[row[j]], 1);
+                for (int j = lane; j < c.max_pages; j += 32) out[j] = -1;
+            }
+            if (at >= 0 && room) {
+                from = row[full];
+                to = ws.a[at];
+                fill = from >= 0 && from < c.num_pages ? ctx % c.P : 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                if (at >= 0 && room) {
+                    out[full] = to;
+                    c.refs[to] = 1;
+                }
+                c.ctx_len[dst[i]] = room ? ctx : 0;
+            }
+        }
+        if (lane == 0) {
+            ws.b[i] = from;
+            ws.c[i] = to;
+            ws.c[n + i] = fill;
+            if (status) status[i] = !ok ? 2 : (room ? 0 : 1);
+        }
+    }
+}
+
+// One warp per sequence. The exchange makes a sequence that is named twice release its pages once.
+__global__ void kv_free_kernel(const CacheArgs c, const int32_t *seqs, int n) {
+    const int i = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    if (i >= n) return;
+    const int s = seqs[i];
+    if (s < 0 || s >= c.S) return;
+    int ctx = 0;
+    if (lane == 0) ctx = atomicExch(&c.ctx_len[s], 0);
+    ctx = __shfl_sync(0xffffffffu, ctx, 0);
+    if (ctx <= 0) return;
+    const int held = pages_of(ctx, c.P, c.max_pages);
+    int32_t *row = c.table + (size_t)s * c.max_pages;
+    for (int j = lane; j < c.max_pages; j += 32) {
+        const int p = row[j];
+        if (j < held && p >= 0 && p < c.num_pages) atomicSub(&c.refs[p], 1);
+        row[j] = -1;
+    }
+}
+
+// a: target, b: source of each move; c[p]: the new id of a page p >= n_live.
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(int32_t *refs, int num_pages, int32_t *n_live_out,
+                                                                      Lists ws) {
+    __shared__ ScanSmem sm;
+    const int tid = threadIdx.x;
+    int mine = 0, n_live;
+    for (int p = tid; p < num_pages; p += kPlanThreads) mine += refs[p] > 0;
+    block_scan(mine, n_live, sm);
+    int gaps = 0, movers = 0;
+    for (int p0 = 0; p0 < num_pages; p0 += 4 * kPlanThreads) {
+        const int p = p0 + 4 * tid;
+        int gap[4], move[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = p + i < num_pages, live = in && refs[p + i] > 0;
+            gap[i] = in && !live && p + i < n_live;
+            move[i] = live && p + i >= n_live;
+            if (in && !live && p + i >= n_live) ws.c[p + i] = p + i;  // an id that a table should not hold stays
+        }
+        // both counts in one scan: pages of one trip number at most 4096, so 16 bits hold each
+        int total;
+        const int at = block_scan((gap[0] + gap[1] + gap[2] + gap[3]) | (move[0] + move[1] + move[2] + move[3]) << 16, total, sm);
+        int g = gaps + (at & 0xffff), m = movers + (at >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (gap[i]) ws.a[g++] = p + i;
+            if (move[i]) ws.b[m++] = p + i;
+        }
+        gaps += total & 0xffff;
+        movers += total >> 16;
+    }
+    __syncthreads();
+    for (int i = tid; i < movers; i += kPlanThreads) {  // as many movers as gaps
+        const int to = ws.a[i], from = ws.b[i];
+        refs[to] = refs[from];
+        refs[from] = 0;
+        ws.c[from] = to;
+    }
+    if (tid == 0) {
+        *ws.count = movers;
+        ws.count[1] = n_live;
+        if (n_live_out) *n_live_out = n_live;
+    }
+}
+
+// ------------------------------------------------------------------ data movement (the whole GPU)
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;  // 16-byte loads in flight per thread
+
+__device__ __forceinline__ void copy_span(unsigned char *dst, const unsigned char *src, int vecs, int part) {
+    uint4 v[kCopyUnroll];
+    const int v0 = part * kCopyThreads * kCopyUnroll + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u)
+        if (v0 + u * kCopyThreads < vecs) v[u] = __ldcs(reinterpret_cast<const uint4 *>(src) + v0 + u * kCopyThreads);
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u)
+        if (v0 + u * kCopyThreads < vecs) __stcs(reinterpret_cast<uint4 *>(dst) + v0 + u * kCopyThreads, v[u]);
+}
+
+// Whole pages src[i] -> dst[i] of every pool; n_dev, when given, is the device's count. Work item: (pool, i, part).
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ PoolPtrs pools, int n_pools, const int32_t *src,
+                                                               const int32_t *dst, int n, const int32_t *n_dev, int num_pages,
+                                                               int page_vecs, int parts) {
+    if (n_dev) n = min(n, *n_dev);
+    const long long items = (long long)n_pools * n * parts;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int part = (int)(it % parts);
+        const long long r = it / parts;
+        const int i = (int)(r % n), pool = (int)(r / n);
+        const int from = src[i], to = dst[i];
+        if (from < 0 || from >= num_pages || to < 0 || to >= num_pages || from == to) continue;
+        copy_span(pools.p[pool] + (size_t)to * page_vecs * 16, pools.p[pool] + (size_t)from * page_vecs * 16, page_vecs, part);
+    }
+}
+
+// The first `fill` rows of every head of page from[i] -> page to[i] in every pool. Work item: (pool, i, part of the page);
+// the filled rows of the heads of a page are numbered one after the other.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid_constant__ PoolPtrs pools, int n_pools,
+                                                                    const int32_t *from, const int32_t *to, const int32_t *fill, int n,
+                                                                    int Hkv, int P, int row_vecs, int parts) {
+    const long long items = (long long)n_pools * n * parts;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int part = (int)(it % parts);
+        const long long r = it / parts;
+        const int i = (int)(r % n), pool = (int)(r / n);
+        const int span = fill[i] * row_vecs;  // 16-byte vectors of one head
+        const int vecs = span * Hkv;
+        if (part * kCopyThreads * kCopyUnroll >= vecs) continue;
+        const uint4 *s = reinterpret_cast<const uint4 *>(pools.p[pool]) + (size_t)from[i] * Hkv * P * row_vecs;
+        uint4 *d = reinterpret_cast<uint4 *>(pools.p[pool]) + (size_t)to[i] * Hkv * P * row_vecs;
+        uint4 v[kCopyUnroll];
+        size_t at[kCopyUnroll];
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u) {
+            const int x = (part * kCopyUnroll + u) * kCopyThreads + threadIdx.x;
+            if (x < vecs) {
+                at[u] = (size_t)(x / span) * P * row_vecs + x % span;
+                v[u] = __ldcs(s + at[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if ((part * kCopyUnroll + u) * kCopyThreads + (int)threadIdx.x < vecs) __stcs(d + at[u], v[u]);
+    }
+}
+
+// Table entries of held pages at or above n_live take the page's new id.
+__global__ void kv_remap_kernel(const CacheArgs c, Lists ws) {
+    const int n_live = ws.count[1];
+    const long long n = (long long)c.S * c.max_pages;
+    for (long long x = blockIdx.x * (long long)blockDim.x + threadIdx.x; x < n; x += (long long)gridDim.x * blockDim.x) {
+        const int s = (int)(x / c.max_pages), j = (int)(x % c.max_pages);
+        if (j >= pages_of(c.ctx_len[s], c.P, c.max_pages)) continue;
+        const int p = c.table[x];
+        if (p >= n_live && p < c.num_pages) c.table[x] = ws.c[p];
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+static int check_pools(const char *what, void *const *pools, int n_pools, int num_pages, int Hkv, int P, int D) {
+    if (!pools) return fail(I4_EINVAL, "%s: null pointer", what);
+    if (n_pools < 1 || num_pages < 1 || num_pages > kMaxPages || Hkv < 1 || P < 1 || D < 8 || D % 8 ||
+        (long long)Hkv * P * D > (1 << 24))
+        return fail(I4_EINVAL, "%s: bad sizes (pools %d, pages %d, Hkv %d, page_size %d, D %d)", what, n_pools, num_pages, Hkv, P,
+                    D);
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i]) return fail(I4_EINVAL, "%s: pool %d is null", what, i);
+        if (!aligned(pools[i], 16)) return fail(I4_EALIGN, "%s: pool %d must be 16-byte aligned", what, i);
+    }
+    return I4_OK;
+}
+
+static int check_cache(const char *what, const i4_kv_cache *c) {
+    if (!c || !c->page_table || !c->ctx_len || !c->refs) return fail(I4_EINVAL, "%s: null pointer", what);
+    if (c->n_seqs < 1 || c->max_pages_per_seq < 1 || c->page_size < 1 || c->num_pages < 1 || c->num_pages > kMaxPages ||
+        (long long)c->max_pages_per_seq * c->page_size > 0x7fffffffll)
+        return fail(I4_EINVAL, "%s: bad sizes (sequences %d, pages per sequence %d, page_size %d, pages %d)", what, c->n_seqs,
+                    c->max_pages_per_seq, c->page_size, c->num_pages);
+    if (c->n_seqs > kMaxSeqs) return fail(I4_EUNSUPPORTED, "%s: %d sequences (at most %d)", what, c->n_seqs, kMaxSeqs);
+    if (!aligned(c->page_table, 4) || !aligned(c->ctx_len, 4) || !aligned(c->refs, 4))
+        return fail(I4_EALIGN, "%s: page_table, ctx_len and refs must be 4-byte aligned", what);
+    return I4_OK;
+}
+
+static int check_list(const char *what, int n, const void *a, const void *b) {
+    if (n < 0 || n > kMaxSeqs) return fail(I4_EINVAL, "%s: %d entries (0 to %d)", what, n, kMaxSeqs);
+    if (n && (!a || !b)) return fail(I4_EINVAL, "%s: null pointer", what);
+    if (!aligned(a, 4) || !aligned(b, 4)) return fail(I4_EALIGN, "%s: lists must be 4-byte aligned", what);
+    return I4_OK;
+}
+
+static size_t ws_cap(int num_pages, int n_seqs) { return (size_t)num_pages + 2 * (size_t)n_seqs; }
+
+static int check_ws(const char *what, void *ws, size_t bytes, int num_pages, int n_seqs) {
+    const size_t need = i4_kv_pages_ws_bytes(num_pages, n_seqs);
+    if (!ws || bytes < need) return fail(I4_EINVAL, "%s: workspace of %zu bytes needed (got %zu)", what, need, bytes);
+    if (!aligned(ws, 16)) return fail(I4_EALIGN, "%s: workspace must be 16-byte aligned", what);
+    return I4_OK;
+}
+
+static CacheArgs cache_args(const i4_kv_cache *c) {
+    return {c->page_table, c->ctx_len, c->refs, c->n_seqs, c->max_pages_per_seq, c->page_size, c->num_pages};
+}
+
+// The plan kernels keep one int per sequence in dynamic shared memory, above 48 KB from 12289 sequences on; the attribute
+// belongs to the current device, and setting it again costs little beside a launch.
+template <typename K>
+static int owner_smem(K kernel, int n_seqs, size_t *bytes, const char *what) {
+    *bytes = (size_t)n_seqs * sizeof(int);
+    if (*bytes <= 47 * 1024) return I4_OK;
+    return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes), what);
+}
+
+static int copy_grid(long long items) {
+    const long long most = 16ll * kNumSMs;
+    return (int)(items < most ? (items > 0 ? items : 1) : most);
+}
+
+static int launch_copy(void *const *pools, int n_pools, const int32_t *src, const int32_t *dst, int n, const int32_t *n_dev,
+                       int num_pages, long long page_bytes, cudaStream_t stream, const char *what) {
+    const int vecs = (int)(page_bytes / 16), parts = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
+    for (int p0 = 0; p0 < n_pools; p0 += kPoolsPerLaunch) {
+        PoolPtrs pp;
+        const int m = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
+        for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
+        kv_copy_kernel<<<copy_grid((long long)m * n * parts), kCopyThreads, 0, stream>>>(pp, m, src, dst, n, n_dev, num_pages, vecs,
+                                                                                       parts);
+        const int st = launch_check(what);
+        if (st) return st;
+    }
+    return I4_OK;
+}
+
+}  // namespace i4
+
+using namespace i4;
+
+extern "C" size_t i4_kv_pages_ws_bytes(int num_pages, int n_seqs) {
+    if (num_pages < 1 || num_pages > kMaxPages || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
+    return (64 + 3 * ws_cap(num_pages, n_seqs)) * sizeof(int32_t);
+}
+
+extern "C" int i4_kv_pages_copy(void *const *pools, int n_pools, int num_pages, int Hkv, int page_size, int D, const int32_t *src,
+                                const int32_t *dst, int n, void *stream) {
+    int st = check_pools("i4_kv_pages_copy", pools, n_pools, num_pages, Hkv, page_size, D);
+    if (st) return st;
+    if (n < 0 || n > kMaxPages) return fail(I4_EINVAL, "i4_kv_pages_copy: %d pages", n);
+    if (n == 0) return I4_OK;
+    if (!src || !dst) return fail(I4_EINVAL, "i4_kv_pages_copy: null pointer");
+    if (!aligned(src, 4) || !aligned(dst, 4)) return fail(I4_EALIGN, "i4_kv_pages_copy: lists must be 4-byte aligned");
+    return launch_copy(pools, n_pools, src, dst, n, nullptr, num_pages, (long long)Hkv * page_size * D * 2, (cudaStream_t)stream,
+                       "i4_kv_pages_copy");
+}
+
+extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs, const int32_t *add, int n, int32_t *status, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    int st = check_cache("i4_kv_pages_reserve", cache);
+    if (!st) st = check_list("i4_kv_pages_reserve", n, seqs, add);
+    if (!st) st = check_ws("i4_kv_pages_reserve", ws, ws_bytes, cache->num_pages, cache->n_seqs);
+    if (st || n == 0) return st;
+    if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_reserve: %d requests for %d sequences", n, cache->n_seqs);
+    size_t smem;
+    if ((st = owner_smem(kv_reserve_kernel, cache->n_seqs, &smem, "i4_kv_pages_reserve"))) return st;
+    kv_reserve_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), seqs, add, n, status,
+                                                                       ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs)));
+    return launch_check("i4_kv_pages_reserve");
+}
+
+extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, const int32_t *src,
+                                const int32_t *dst, int n, int32_t *status, void *ws, size_t ws_bytes, void *stream) {
+    int st = check_cache("i4_kv_pages_fork", cache);
+    if (!st) st = check_pools("i4_kv_pages_fork", pools, n_pools, cache->num_pages, Hkv, cache->page_size, D);
+    if (!st) st = check_list("i4_kv_pages_fork", n, src, dst);
+    if (!st) st = check_ws("i4_kv_pages_fork", ws, ws_bytes, cache->num_pages, cache->n_seqs);
+    if (st || n == 0) return st;
+    if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_fork: %d forks for %d sequences", n, cache->n_seqs);
+    size_t smem;
+    if ((st = owner_smem(kv_fork_kernel, cache->n_seqs, &smem, "i4_kv_pages_fork"))) return st;
+    const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
+    kv_fork_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), src, dst, n, status, L);
+    if ((st = launch_check("i4_kv_pages_fork"))) return st;
+    const int row_vecs = D / 8, vecs = Hkv * cache->page_size * row_vecs;
+    const int parts = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
+    for (int p0 = 0; p0 < n_pools; p0 += kPoolsPerLaunch) {
+        PoolPtrs pp;
+        const int m = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
+        for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
+        kv_copy_rows_kernel<<<copy_grid((long long)m * n * parts), kCopyThreads, 0, (cudaStream_t)stream>>>(
+            pp, m, L.b, L.c, L.c + n, n, Hkv, cache->page_size, row_vecs, parts);
+        if ((st = launch_check("i4_kv_pages_fork copy"))) return st;
+    }
+    return I4_OK;
+}
+
+extern "C" int i4_kv_pages_free(const i4_kv_cache *cache, const int32_t *seqs, int n, void *stream) {
+    int st = check_cache("i4_kv_pages_free", cache);
+    if (!st) st = check_list("i4_kv_pages_free", n, seqs, seqs);
+    if (st || n == 0) return st;
+    kv_free_kernel<<<(n + 3) / 4, 128, 0, (cudaStream_t)stream>>>(cache_args(cache), seqs, n);
+    return launch_check("i4_kv_pages_free");
+}
+
+extern "C" int i4_kv_pages_compact(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, int32_t *n_live, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    int st = check_cache("i4_kv_pages_compact", cache);
+    if (!st) st = check_pools("i4_kv_pages_compact", pools, n_pools, cache->num_pages, Hkv, cache->page_size, D);
+    if (!st) st = check_ws("i4_kv_pages_compact", ws, ws_bytes, cache->num_pages, cache->n_seqs);
+    if (st) return st;
+    const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
+    kv_compact_plan_kernel<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(cache->refs, cache->num_pages, n_live, L);
+    if ((st = launch_check("i4_kv_pages_compact plan"))) return st;
+    const long long entries = (long long)cache->n_seqs * cache->max_pages_per_seq;
+    kv_remap_kernel<<<copy_grid((entries + 255) / 256), 256, 0, (cudaStream_t)stream>>>(cache_args(cache), L);
+    if ((st = launch_check("i4_kv_pages_compact tables"))) return st;
+    return launch_copy(pools, n_pools, L.b, L.a, cache->num_pages, L.count, cache->num_pages,
+                       (long long)Hkv * cache->page_size * D * 2, (cudaStream_t)stream, "i4_kv_pages_compact");
+}
