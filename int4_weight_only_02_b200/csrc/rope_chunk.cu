@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
     const int b = chunk_find(p.q_start, p.B, t);
     if (b >= p.B) return;  // a row behind the last sequence
     const int2 rows = chunk_rows(p.q_start, b, p.T);
-    const int pos = p.ctx_len[b] - rows.y + (t - rows.x);
+    const int pos = max(p.ctx_len[b], 0) - rows.y + (t - rows.x);
     if (t < rows.x || pos < 0 || pos >= p.max_pos || pos / p.page_size >= p.max_pages) return;
     const int page = p.page_table[(size_t)b * p.max_pages + pos / p.page_size], slot = pos % p.page_size;
     const bool page_ok = page >= 0 && page < p.num_pages;
