@@ -6,10 +6,10 @@
 // sum of the softmax.
 //
 //  * Rows. The G = Hq / Hkv query heads that share a kv head are rows of one
-//    matrix: row r of a sequence is (token r / G, head r % G), so 128 rows (the M of an
-//    MMA) are 128 / G consecutive tokens, every K/V tile is read once for all of them, and a
-//    short chunk fills the rows better than one head's tokens would.
-//  * Work. A unit is NQ * 128 rows of one sequence and one kv head; its cost is the
+//    matrix: row r of a slot is (token r / G, head r % G), so the 128 rows of an MMA are 128 / G (rounded down)
+//    consecutive tokens, every K/V tile is read once for all of them, and a short chunk fills the rows better than one head's
+//    tokens would. One TMA box of (64 dims, G heads, 128 / G tokens) brings half of a slot's Q in that order.
+//  * Work. A unit is NQ slots' tokens of one sequence and one kv head; its cost is the
 //    number of 128-position tiles that its rows see. The units stand in one line (kv heads
 //    outermost) and every CTA, one or two per SM, takes an equal stretch of the line's tiles, whatever
 //    unit borders lie in it: a prompt's long and short units balance, and a
@@ -41,16 +41,20 @@ constexpr int kTile = 128;                         // positions of a K/V tile
 constexpr unsigned kHalf = kTile * 128;            // 64 of the 128 dims of a tile, 128 bytes per row
 constexpr unsigned kTileBytes = 2 * kHalf;         // 32 KB
 constexpr int kMaxCtas = 2 * kNumSMs;
-constexpr int kMinTiles = 2;                       // tiles that are worth a CTA of their own
 constexpr float kGrow = 8.f;                       // powers of two that a row's maximum may run ahead of its m
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFma = 4;
 
 template <int NQ>
 struct Cfg {
-    static constexpr int kThreads = NQ * 128 + 64;  // softmax warpgroups, the MMA warp, the load warp
+    // softmax warpgroups, an MMA warp each, the load warp; with NQ = 2 an idle warp fills the last warpgroup, which
+    // hands registers to the others (setmaxnreg): 256 * 208 + 128 * 88 = 384 * 168
+    static constexpr int kThreads = NQ == 2 ? 384 : 192;
     static constexpr int kStages = NQ == 2 ? 5 : 2;
     static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
     static constexpr int kUnitRows = NQ * kRows;
+    static constexpr int kUnitCost = 1;  // what beginning and ending a unit costs, in tiles
+    static constexpr int kMinCost = 2;   // tiles that are worth a CTA of their own
     static constexpr unsigned kTmemCols = NQ * 256;  // S / P and O of every slot
     static constexpr unsigned kSmem = 1024 + (NQ + kStages) * kTileBytes;
 };
@@ -59,7 +63,7 @@ __device__ int g_chunk_error = 0;
 
 // Where a unit is cut at the beginning of a CTA's stretch: what the joining kernel needs.
 struct Cut {
-    int valid, last, rows, row0, r0, g;  // parts: CTA c-1's last, then the first of c .. last; unit rows [r0, r0 + rows)
+    int valid, last, tokens, row, g;  // parts: CTA c-1's last, then the first of c .. last; the unit's tokens begin at this row of q
 };
 
 struct ChunkAttnParams {
@@ -69,17 +73,18 @@ struct ChunkAttnParams {
     uint16_t *out;
     int T, B, Hq, Hkv, page_size, max_pages, num_pages, window;
     float scale;
+    int slot_tokens;  // 128 / G
     Cut *cuts;        // [kMaxCtas]
     float2 *part_ml;  // [2 * CTAs][unit rows]: (m in powers of two, l)
-    float4 *part_o;   // [2 * CTAs][unit rows / 32][32 column quads][32 rows]
+    float *part_o;    // [2 * CTAs][unit rows][128]
 };
 
 // ------------------------------------------------------------------ the line of units
 
-// Positions that the rows [r, e) of a sequence with n tokens from position pos0 on may see: [x, y), empty when y <= x.
-__device__ __forceinline__ int2 seen(const ChunkAttnParams &p, int pos0, int G, int r, int e) {
-    const int hi = min(pos0 + (e - 1) / G + 1, p.max_pages * p.page_size);
-    const int lo = p.window > 0 ? max(0, pos0 + r / G - p.window + 1) : 0;
+// Positions that the tokens [a, e) of a sequence whose first new token stands at pos0 may see: [x, y), empty when y <= x.
+__device__ __forceinline__ int2 seen(const ChunkAttnParams &p, int pos0, int a, int e) {
+    const int hi = min(pos0 + e, p.max_pages * p.page_size);
+    const int lo = p.window > 0 ? max(0, pos0 + a - p.window + 1) : 0;
     return make_int2(lo, hi);
 }
 __device__ __forceinline__ int2 tiles_of(int2 s) {
@@ -88,14 +93,15 @@ __device__ __forceinline__ int2 tiles_of(int2 s) {
 
 // A CTA's stretch of the line.
 struct Stretch {
-    int g, b, i, off;  // first unit, and its tiles that belong to earlier CTAs
-    int left;          // tiles of the stretch (a unit that sees nothing counts as one)
+    int g, b, i, off;  // first unit, and what of its cost belongs to earlier CTAs
+    int left;          // cost of the stretch
+    int n, pos0, row0; // the first unit's sequence
 };
 
 // One unit's part in a stretch.
 struct Piece {
-    int g, b, n, pos0, row0;  // kv head; sequence: tokens, first position, first row of q
-    int r0, rows;             // the unit's rows of the sequence
+    int g, b, pos0, row0;     // kv head; sequence: first position, first row of q
+    int tok0, tokens;         // the unit's tokens of the sequence
     int2 see;                 // positions that the unit sees
     int t0, t1;               // the part's tiles
     int whole, slot;          // uncut, or the slot of its parts
@@ -105,58 +111,63 @@ struct Piece {
 template <int NQ>
 struct Walker {
     const ChunkAttnParams &p;
-    const int G;
+    const int unit;  // tokens of a unit
     int g, b, i, off, left, n, pos0, row0, units;
     __device__ Walker(const ChunkAttnParams &p_, const Stretch &s)
-        : p(p_), G(p_.Hq / p_.Hkv), g(s.g), b(s.b), i(s.i), off(s.off), left(s.left) {
-        if (left > 0) load();
+        : p(p_), unit(NQ * p_.slot_tokens), g(s.g), b(s.b), i(s.i), off(s.off), left(s.left), n(s.n), pos0(s.pos0),
+          row0(s.row0) {
+        units = (n + unit - 1) / unit;
     }
     __device__ void load() {
         const int2 r = chunk_rows(p.q_start, b, p.T);
         row0 = r.x;
         n = r.y;
         pos0 = max(p.ctx_len[b], 0) - n;
-        units = (n * G + Cfg<NQ>::kUnitRows - 1) / Cfg<NQ>::kUnitRows;
+        units = (n + unit - 1) / unit;
     }
     __device__ bool next(Piece &pc) {
-        if (left <= 0) return false;
-        pc.g = g;
-        pc.b = b;
-        pc.n = n;
-        pc.pos0 = pos0;
-        pc.row0 = row0;
-        pc.r0 = i * Cfg<NQ>::kUnitRows;
-        pc.rows = min(n * G - pc.r0, Cfg<NQ>::kUnitRows);
-        pc.see = seen(p, pos0, G, pc.r0, pc.r0 + pc.rows);
-        const int2 t = tiles_of(pc.see);
-        const int cost = max(t.y - t.x, 1), take = min(cost - off, left);
-        pc.t0 = t.x + off;
-        pc.t1 = min(t.y, pc.t0 + take);
-        pc.whole = take == cost;
-        pc.slot = 2 * blockIdx.x + (off == 0);
-        left -= take;
-        off = 0;
-        if (left > 0 && ++i == units) {
-            i = 0;
-            do {
-                if (++b == p.B) {
-                    b = 0;
-                    ++g;
-                }
-                load();
-            } while (units == 0);
+        constexpr int V = Cfg<NQ>::kUnitCost;  // a unit's cost lies on the line as V, then its tiles
+        while (left > 0) {
+            pc.g = g;
+            pc.b = b;
+            pc.pos0 = pos0;
+            pc.row0 = row0;
+            pc.tok0 = i * unit;
+            pc.tokens = min(n - pc.tok0, unit);
+            pc.see = seen(p, pos0, pc.tok0, pc.tok0 + pc.tokens);
+            const int2 t = tiles_of(pc.see);
+            const int tiles = t.y - t.x, take = min(tiles + V - off, left);
+            const int x = max(off - V, 0), y = max(off + take - V, 0);
+            const bool any = tiles > 0 ? y > x : off == 0;  // rows that see nothing are written by one CTA too
+            pc.t0 = t.x + x;
+            pc.t1 = t.x + y;
+            pc.whole = y - x == tiles;
+            pc.slot = 2 * blockIdx.x + (x == 0);
+            left -= take;
+            off = 0;
+            if (left > 0 && ++i == units) {
+                i = 0;
+                do {
+                    if (++b == p.B) {
+                        b = 0;
+                        ++g;
+                    }
+                    load();
+                } while (units == 0);
+            }
+            if (any) return true;
         }
-        return true;
+        return false;
     }
 };
 
-// Tiles of a piece that the rows of slot s see: [x, y), and how many rows it has.
-__device__ __forceinline__ int3 slot_tiles(const ChunkAttnParams &p, int G, const Piece &pc, int s) {
-    const int rows = min(max(pc.rows - s * kRows, 0), kRows);
-    if (rows == 0) return make_int3(0, 0, 0);
-    const int2 t = tiles_of(seen(p, pc.pos0, G, pc.r0 + s * kRows, pc.r0 + s * kRows + rows));
+// Tiles of a piece that the tokens of slot s see: [x, y), and how many tokens it has.
+__device__ __forceinline__ int3 slot_tiles(const ChunkAttnParams &p, const Piece &pc, int s) {
+    const int a = pc.tok0 + s * p.slot_tokens, n = min(max(pc.tokens - s * p.slot_tokens, 0), p.slot_tokens);
+    if (n == 0) return make_int3(0, 0, 0);
+    const int2 t = tiles_of(seen(p, pc.pos0, a, a + n));
     const int x = max(t.x, pc.t0), y = min(t.y, pc.t1);
-    return y > x ? make_int3(x, y, rows) : make_int3(0, 0, rows);
+    return y > x ? make_int3(x, y, n) : make_int3(0, 0, n);
 }
 
 template <int NT>
@@ -181,26 +192,45 @@ __device__ __forceinline__ int scan_block(int v, int &total, int *warp_sums) {
     return before + inc - v;
 }
 
-// This CTA's stretch (out, thread 0's view in shared memory) and the cut at its beginning. scratch: NT + 32 ints.
+// This CTA's stretch, and the cut at its beginning. scratch: 32 + 3 NT ints of shared memory.
 template <int NQ>
 __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *out, int *scratch) {
-    constexpr int NT = Cfg<NQ>::kThreads, R = Cfg<NQ>::kUnitRows;
-    const int tid = threadIdx.x, G = p.Hq / p.Hkv;
-    int *sums = scratch, *first = scratch + 32;  // first[j]: units before sequence b0 + j
-    if (tid == 0) *out = {0, 0, 0, 0, 0};
-    long long W = 0, start = 0, end = 0;
-    int n_ctas = 1, line = 0, target = 0;
+    constexpr int NT = Cfg<NQ>::kThreads, V = Cfg<NQ>::kUnitCost;
+    const int tid = threadIdx.x, size = NQ * p.slot_tokens;
+    int *sums = scratch, *first = scratch + 32, *tokens = first + NT, *pos = tokens + NT;  // units before sequence b0 + j; the sequence
+    if (tid == 0) *out = {0, 0, 0, 0, 0, 0, 0, 0};
+    long long W = 0, start = 0;
+    int n_ctas = 1, line = 0, target = 0, length = 0;
+    int cost = 0, at = 0, j = 0, i = 0;  // this thread's unit: unit i of sequence b0 + j
+    auto place = [&](int b0) {
+        if (cost == 0 || target < at || target >= at + cost) return;
+        const int g = (int)(start / line), off = target - at;
+        const int2 seq = chunk_rows(p.q_start, b0 + j, p.T);
+        *out = {g, b0 + j, i, off, length, seq.y, pos[j], seq.x};
+        Cut cut = {0, 0, 0, 0, 0};
+        const long long unit = start - off;  // where the unit begins
+        if (off > V && W * (blockIdx.x - 1) / n_ctas <= unit + V) {
+            // the first cut of this unit: its parts end in the CTA that holds its last tile
+            cut = {1, (int)(((unit + cost) * n_ctas - 1) / W), min(seq.y - i * size, size), seq.x + i * size, g};
+        }
+        p.cuts[blockIdx.x] = cut;
+    };
     for (int pass = 0; pass < 2; ++pass) {  // the first measures the line, the second finds the place in it
-        int run = 0;
+        int run = 0, trips = 0;
         for (int b0 = 0; b0 < p.B; b0 += NT) {
-            int nu = 0, total_units;
-            if (b0 + tid < p.B) nu = (chunk_rows(p.q_start, b0 + tid, p.T).y * G + R - 1) / R;
-            const int before = scan_block<NT>(nu, total_units, sums);
+            int n = 0, first_pos = 0, total_units;
+            if (b0 + tid < p.B) {
+                n = chunk_rows(p.q_start, b0 + tid, p.T).y;
+                first_pos = max(p.ctx_len[b0 + tid], 0) - n;
+            }
+            const int before = scan_block<NT>((n + size - 1) / size, total_units, sums);
             first[tid] = before;
+            tokens[tid] = n;
+            pos[tid] = first_pos;
             __syncthreads();
-            for (int u0 = 0; u0 < total_units; u0 += NT) {
+            for (int u0 = 0; u0 < total_units; u0 += NT, ++trips) {
                 const int u = u0 + tid;
-                int cost = 0, j = 0, i = 0;
+                cost = j = 0;
                 if (u < total_units) {
                     int len = min(NT, p.B - b0);  // the last sequence whose first unit is not behind u
                     while (len > 1) {
@@ -213,39 +243,31 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
                         }
                     }
                     i = u - first[j];
-                    const int n = chunk_rows(p.q_start, b0 + j, p.T).y, r0 = i * R;
-                    const int2 t = tiles_of(seen(p, max(p.ctx_len[b0 + j], 0) - n, G, r0, min(n * G, r0 + R)));
-                    cost = max(t.y - t.x, 1);
+                    const int2 t = tiles_of(seen(p, pos[j], i * size, min(tokens[j], i * size + size)));
+                    cost = t.y - t.x + V;
                 }
                 int sum;
-                const int at = run + scan_block<NT>(cost, sum, sums);
-                if (pass == 1 && cost > 0 && target >= at && target < at + cost) {
-                    const int g = (int)(start / line), off = target - at;
-                    *out = {g, b0 + j, i, off, (int)(end - start)};
-                    Cut cut = {0, 0, 0, 0, 0, 0};
-                    const long long unit = start - off;  // where the unit begins
-                    if (off > 0 && W * (blockIdx.x - 1) / n_ctas <= unit) {
-                        // the first cut of this unit: its parts end in the CTA that holds its last tile
-                        const int2 rows = chunk_rows(p.q_start, b0 + j, p.T);
-                        cut = {1, (int)(((unit + cost) * n_ctas - 1) / W), min(rows.y * G - i * R, R), rows.x, i * R, g};
-                    }
-                    p.cuts[blockIdx.x] = cut;
-                }
+                at = run + scan_block<NT>(cost, sum, sums);
+                if (pass == 1) place(b0);
                 run += sum;
             }
-            __syncthreads();  // first[] is read no more
+            __syncthreads();  // the scratch is read no more
         }
         if (pass == 0) {
             line = run;
             W = (long long)line * p.Hkv;
-            n_ctas = (int)min((long long)gridDim.x, max((W + kMinTiles - 1) / kMinTiles, 1ll));
+            n_ctas = (int)min((long long)gridDim.x, max((W + Cfg<NQ>::kMinCost - 1) / Cfg<NQ>::kMinCost, 1ll));
             start = W * blockIdx.x / n_ctas;
-            end = W * (blockIdx.x + 1) / n_ctas;
-            if ((int)blockIdx.x >= n_ctas || start >= end) {
+            length = (int)(W * (blockIdx.x + 1) / n_ctas - start);
+            if ((int)blockIdx.x >= n_ctas || length <= 0) {
                 if (tid == 0) p.cuts[blockIdx.x].valid = 0;
                 break;
             }
             target = (int)(start % line);
+            if (trips == 1 && p.B <= NT) {  // every unit is still in its thread's hands
+                place(0);
+                break;
+            }
         }
     }
     __syncthreads();
@@ -258,6 +280,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// 2^x for two values on the FMA units: x = n + f with n the nearest integer (Cody and Waite's reduction, by adding
+// and taking away 1.5 * 2^23), a polynomial for 2^f on [-1/2, 1/2] (degree 4, least relative maximum error, own fit:
+// 2.7e-6 in fp32), and n added to the exponent. x below -126 gives less than 2^-125, which is zero in fp16.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    const float2 big = make_float2(12582912.f, 12582912.f), none = make_float2(-1.f, -1.f);
+    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    const float2 t = fadd2(x, big);
+    const float2 f = fadd2(x, ffma2(t, none, big));
+    float2 y = ffma2(f, make_float2(0.00957010221f, 0.00957010221f), make_float2(0.0559178703f, 0.0559178703f));
+    y = ffma2(y, f, make_float2(0.240247443f, 0.240247443f));
+    y = ffma2(y, f, make_float2(0.693121791f, 0.693121791f));
+    y = ffma2(y, f, make_float2(0.999999285f, 0.999999285f));
+    return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// A value that is the same in every lane of the warp, in a form that the compiler knows to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A wait that ends: on the barrier, when another role of the CTA gave up, or after ~2 s.
 __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, unsigned parity, volatile int *stop) {
@@ -272,6 +320,28 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, unsigned parity, vol
         }
     }
     return true;
+}
+
+// v[i] of lane 4a + k becomes v[k] of lane 4a + i.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
+    const int lane = threadIdx.x & 3;
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            uint4 give = up ? v[i] : v[i + d];
+            give.x = __shfl_xor_sync(0xffffffffu, give.x, d);
+            give.y = __shfl_xor_sync(0xffffffffu, give.y, d);
+            give.z = __shfl_xor_sync(0xffffffffu, give.z, d);
+            give.w = __shfl_xor_sync(0xffffffffu, give.w, d);
+            if (up)
+                v[i] = give;
+            else
+                v[i + d] = give;
+        }
+    }
 }
 
 // The sum over the positions [lo, hi) of one row by plain loads, for rows whose tensor-core sum met a NaN or an
@@ -299,12 +369,12 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
 
 template <int NQ>
 __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
-    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ ChunkAttnParams p) {
     using C = Cfg<NQ>;
-    constexpr int S = C::kStages, kMmaWarp = NQ * 4, kLoadWarp = NQ * 4 + 1;
+    constexpr int S = C::kStages, kMmaWarp = NQ * 4, kLoadWarp = kMmaWarp + NQ;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], s_full[NQ], p_full[NQ], o_full[NQ], o_free[NQ], all_done;
+    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], q_free[NQ], s_full[NQ], p_half[NQ], p_full[NQ], o_full[NQ], o_free[NQ], turn[NQ], all_done;
     __shared__ uint32_t tmem_base;
     __shared__ Stretch stretch;
     __shared__ int stop_flag;
@@ -315,23 +385,23 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     unsigned char *gbase = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t ring = base + NQ * kTileBytes;
 
-    find_stretch<NQ>(p, &stretch, reinterpret_cast<int *>(gbase));
-    grid_dep_launch();  // the joining kernel may come up; it waits for this grid's end before it reads anything
-    if (stretch.left <= 0) return;
     if (tid == 0) {
         stop_flag = 0;
         for (int i = 0; i < S; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_empty[i], NQ);
         }
         for (int s = 0; s < NQ; ++s) {
-            mbar_init(&q_full[s], 4);
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_free[s], 1);
             mbar_init(&s_full[s], 1);
+            mbar_init(&p_half[s], 4);
             mbar_init(&p_full[s], 4);
             mbar_init(&o_full[s], 1);
             mbar_init(&o_free[s], 4);
+            mbar_init(&turn[s], 1);
         }
-        mbar_init(&all_done, 1);
+        mbar_init(&all_done, NQ);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -340,19 +410,56 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == kLoadWarp && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &tm_q : (lane == 1 ? &tm_k : &tm_v)) : "memory");
+    find_stretch<NQ>(p, &stretch, reinterpret_cast<int *>(gbase));
+    grid_dep_launch();  // the joining kernel may come up; it waits for this grid's end before it reads anything
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = tmem_base;  // S / P of slot s at column 128 s, O of slot s at 128 (NQ + s)
+    const uint32_t tmem = uniform(tmem_base);  // S / P of slot s at column 128 s, O of slot s at 128 (NQ + s)
 
     Walker<NQ> walk(p, stretch);
     Piece pc;
-    if (warp == kLoadWarp) {
+    if (stretch.left <= 0) {
+        // no work: straight to the end
+    } else if (warp >= kMmaWarp) {
+    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // The rows of Q of one slot's piece: tokens behind the sequence's are another's, or zeros behind the last row; nothing
+    // that comes of them is stored.
+    auto load_q = [&](const Piece &c, int s) {
+        if (lane == 0) {
+            mbar_expect_tx(&q_full[s], (unsigned)(p.slot_tokens * G) * 256u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                tma_load_4d(base + s * kTileBytes + h * kHalf, &tm_q, 64 * h, c.g * G, c.row0 + c.tok0 + s * p.slot_tokens, 0, &q_full[s]);
+        }
+    };
+    if (warp > kLoadWarp) {
+        // ---------------- rows of Q (NQ = 2; with NQ = 1 the load warp's own)
+        unsigned uses[NQ] = {};
+        bool ok = true;
+        while (ok && walk.next(pc)) {
+#pragma unroll
+            for (int s = 0; s < NQ; ++s) {
+                const int3 r = slot_tiles(p, pc, s);
+                if (r.y <= r.x) continue;
+                if (ok && uses[s] > 0) ok = wait_or_stop(&q_free[s], (uses[s] - 1) & 1, stop);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) load_q(pc, s);
+                uses[s] += ok;
+            }
+        }
+        if (!ok && lane == 0)  // let the copies in flight land
+            for (int s = 0; s < NQ; ++s)
+                if (uses[s] > 0) mbar_wait(&q_full[s], (uses[s] - 1) & 1);
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
         // ---------------- K and V tiles: K0 V0 K1 V1 ...
         const int np = kTile / p.page_size;  // pages of a tile
         const int half = lane / np, pg = lane % np;
         const bool loads = lane < 2 * np;
-        unsigned it = 0;
+        unsigned it = 0, uses = 0;
         bool ok = true;
         while (ok && walk.next(pc)) {
             for (int t = pc.t0; ok && t < pc.t1; ++t) {
@@ -375,32 +482,47 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     if (loads)
                         tma_load_4d(ring + st * kTileBytes + half * kHalf + pg * p.page_size * 128, kv ? &tm_v : &tm_k, half * 64, 0,
                                     pc.g, page, &kv_full[st]);
+                    if (NQ == 1 && t == pc.t0 && kv == 0) {  // behind the piece's first K tile
+                        if (uses > 0) ok = wait_or_stop(&q_free[0], (uses - 1) & 1, stop);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) {
+                            ++it;
+                            break;
+                        }
+                        load_q(pc, 0);
+                        ++uses;
+                    }
                 }
             }
         }
-        if (!ok)  // let the copies in flight land before the CTA's memory goes
-            for (unsigned k = it > S ? it - S : 0; k < it; ++k)
-                if (lane == 0) mbar_wait(&kv_full[k % S], (k / S) & 1);
+        if (!ok && lane == 0) {  // let the copies in flight land before the CTA's memory goes
+            for (unsigned k = it > S ? it - S : 0; k < it; ++k) mbar_wait(&kv_full[k % S], (k / S) & 1);
+            if (NQ == 1 && uses > 0) mbar_wait(&q_full[0], (uses - 1) & 1);
+        }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---------------- S = Q K^T and O += P V of every slot
+    } else if (warp < kMmaWarp + NQ) {
+        // ---------------- S = Q K^T and O += P V of slot s. One warp per slot: a tile takes a warp some 150 instructions that
+        // nothing else on its scheduler shares, and both slots' in one warp took longer than the tensor cores' own work
         constexpr uint32_t idesc_qk = idesc_f16(kRows, kTile), idesc_pv = idesc_f16(kRows, 128) | kIdescBMajorMN;
-        unsigned it = 0, uses[NQ], steps[NQ];  // pieces and tiles of every slot so far
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) uses[s] = steps[s] = 0;
+        const int s = (int)uniform((uint32_t)(warp - kMmaWarp));
+        const uint32_t tP = tmem + 128 * s, tO = tmem + 128 * (NQ + s);
+        const uint64_t qd = desc_sw128(base + s * kTileBytes), kd0 = desc_sw128(ring), vd0 = desc_sw128_mn(ring, kHalf);
+        unsigned it = 0, uses = 0, steps = 0, turns = 0;  // ring entries, pieces, tiles and turns so far
         bool ok = true;
         while (ok && walk.next(pc)) {
-            int3 r[NQ];
-#pragma unroll
-            for (int s = 0; s < NQ; ++s) r[s] = slot_tiles(p, G, pc, s);
-            for (int j = pc.t0 - 1; ok && j < pc.t1; ++j) {
-                if (pc.t1 <= pc.t0) break;
-                const unsigned iv = it + 2 * (j - pc.t0) + 1, ik = iv + 1, sv = iv % S, sk = ik % S;
-                if (j >= pc.t0) {
-                    ok = wait_or_stop(&kv_full[sv], (iv / S) & 1, stop);
+            const int3 r = slot_tiles(p, pc, s);
+            if (pc.t1 <= pc.t0) continue;
+#pragma unroll 1
+            for (int j = pc.t0 - 1; j < pc.t1; ++j, it += 2) {
+                // entries it - 1: V of tile j, it: K of tile j + 1
+                const unsigned sv = (it - 1) % S, sk = it % S;
+                const bool has_v = j >= pc.t0, has_k = j + 1 < pc.t1;
+                if (has_v) {
+                    ok = wait_or_stop(&kv_full[sv], ((it - 1) / S) & 1, stop);
                     const int t = j * kTile;
                     if (ok && (t < pc.see.x || t + kTile > pc.see.y)) {
-                        // rows of V that the unit does not see may hold anything, NaN included: zero them
+                        // rows of V that the unit does not see may hold anything, NaN included: zero them (both slots' warps
+                        // write the same zeros)
                         for (int e = lane; e < 2 * kTile * 8; e += 32) {
                             const int u = (e >> 3) & (kTile - 1);
                             if (t + u < pc.see.x || t + u >= pc.see.y)
@@ -410,84 +532,100 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     }
                     __syncwarp();
                 }
-                if (ok && j + 1 < pc.t1) ok = wait_or_stop(&kv_full[sk], (ik / S) & 1, stop);
-#pragma unroll
-                for (int s = 0; s < NQ; ++s) {
-                    if (ok && j >= r[s].x && j < r[s].y) {
-                        ok = wait_or_stop(&p_full[s], steps[s] & 1, stop);
-                        ++steps[s];
-                        if (ok && j == r[s].x) {
-                            if (uses[s] > 0) ok = wait_or_stop(&o_free[s], (uses[s] - 1) & 1, stop);
-                            ++uses[s];
+                if (ok && has_k) ok = wait_or_stop(&kv_full[sk], (it / S) & 1, stop);
+                const bool pv = j >= r.x && j < r.y;
+                if (ok && pv) ok = wait_or_stop(&p_half[s], steps & 1, stop);
+                if (NQ == 2 && ok && (s == 1 || turns > 0)) ok = wait_or_stop(&turn[s], (turns - (s == 0)) & 1, stop);
+                ++turns;
+                if (has_v) {
+                    if (pv) {
+                        if (ok && j == r.x) {
+                            if (uses > 0) ok = wait_or_stop(&o_free[s], (uses - 1) & 1, stop);
+                            ++uses;
                         }
-                        ok = __all_sync(0xffffffffu, ok);
+                        const uint64_t vd = vd0 + uniform(sv) * (kTileBytes >> 4);
+                        const int more = j > r.x;
+                        if (!__all_sync(0xffffffffu, ok)) break;
                         fence_after_sync();
-                        if (ok && lane == 0) {
-                            const uint32_t tP = tmem + 128 * s, tO = tmem + 128 * (NQ + s), vb = ring + sv * kTileBytes;
+                        if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk)
-                                umma_f16_ta(tO, tP + 8 * kk, desc_sw128_mn(vb + kk * 2048, kHalf), idesc_pv,
-                                            (j > r[s].x || kk > 0) ? 1 : 0);
-                            if (j + 1 == r[s].y) umma_commit(&o_full[s]);
+                            for (int kk = 0; kk < kTile / 32; ++kk)
+                                umma_f16_ta(tO, tP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : more);
                         }
                         __syncwarp();
-                    }
-                    if (ok && j + 1 >= r[s].x && j + 1 < r[s].y) {
-                        if (j + 1 == r[s].x) ok = wait_or_stop(&q_full[s], uses[s] & 1, stop);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = wait_or_stop(&p_full[s], steps & 1, stop);
+                        ++steps;
+                        if (!__all_sync(0xffffffffu, ok)) break;
                         fence_after_sync();
-                        if (ok && lane == 0) {
-                            const uint32_t qb = base + s * kTileBytes, kb = ring + sk * kTileBytes;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = kTile / 32; kk < kTile / 16; ++kk)
+                                umma_f16_ta(tO, tP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, 1);
+                            umma_commit(&kv_empty[sv]);
+                            if (j + 1 == r.y) umma_commit(&o_full[s]);
+                        }
+                        __syncwarp();
+                    } else {
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        if (elect_one()) umma_commit(&kv_empty[sv]);
+                        __syncwarp();
+                    }
+                }
+                if (has_k) {
+                    const bool mine = j + 1 >= r.x && j + 1 < r.y;
+                    if (ok && mine && j + 1 == r.x) ok = wait_or_stop(&q_full[s], uses & 1, stop);
+                    const uint64_t kd = kd0 + uniform(sk) * (kTileBytes >> 4);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    fence_after_sync();
+                    if (elect_one()) {
+                        if (mine) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-                                umma_f16(tmem + 128 * s, desc_sw128(qb + o), desc_sw128(kb + o), idesc_qk, kk > 0 ? 1 : 0);
+                                const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                                umma_f16(tP, qd + o, kd + o, idesc_qk, kk > 0 ? 1 : 0);
                             }
                             umma_commit(&s_full[s]);
+                            if (j + 2 == r.y) umma_commit(&q_free[s]);
                         }
-                        __syncwarp();
+                        umma_commit(&kv_empty[sk]);
                     }
+                    __syncwarp();
                 }
-                if (ok && lane == 0) {
-                    if (j >= pc.t0) umma_commit(&kv_empty[sv]);
-                    if (j + 1 < pc.t1) umma_commit(&kv_empty[sk]);
-                }
-                __syncwarp();
+                if (NQ == 2 && lane == 0) mbar_arrive(&turn[s ^ 1]);
             }
-            it += 2 * (pc.t1 > pc.t0 ? pc.t1 - pc.t0 : 0);
+            ok = __all_sync(0xffffffffu, ok);
+            it -= 2;
         }
-        // nothing of this CTA is in flight on the tensor cores when it leaves
-        if (lane == 0) {
-            umma_commit(&all_done);
-            if (!mbar_wait(&all_done, 0)) record_error(&g_chunk_error, 1);
-        }
+        // nothing of this slot is in flight on the tensor cores when the CTA leaves
+        if (elect_one()) umma_commit(&all_done);
+        if (!mbar_wait(&all_done, 0)) record_error(&g_chunk_error, 1);
         __syncwarp();
+    }
     } else {
         // ---------------- softmax of slot s: thread = row
+        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int s = warp >> 2, wq = warp & 3, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t tS = tmem + 128 * s + lanes, tO = tmem + 128 * (NQ + s) + lanes;
+        const int my_tok = row / G, my_head = row - my_tok * G;  // within the slot and the kv head
         const float qs = p.scale * kLog2e, grow = fminf(kGrow / qs, 1e30f);
         unsigned tiles = 0, pieces = 0;
         bool ok = true;
 
-        // the last piece's results, stored once the next piece's rows of Q are on their way
-        Piece last = {};
-        int3 last_r = make_int3(0, 0, 0);
         float m = -INFINITY, l = 0.f;
         auto limits = [&](const Piece &c, int &lo, int &hi) {  // positions that this thread's row sees
-            const int tok = (c.r0 + s * kRows + row) / G, pos = c.pos0 + tok;
+            const int pos = c.pos0 + c.tok0 + s * p.slot_tokens + my_tok;
             hi = min(pos + 1, p.max_pages * p.page_size);
             lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         };
-        auto finish = [&] {
-            if (last_r.z == 0) return;  // the slot had no rows
-            const bool mine = row < last_r.z, any = last_r.y > last_r.x;
-            const int r = last.r0 + s * kRows + row, tok = r / G, head = last.g * G + r % G;
+        auto finish = [&](const Piece &last, const int3 &last_r) {
+            if (last_r.z == 0) return;  // the slot has no rows
+            const bool mine = my_tok < last_r.z, any = last_r.y > last_r.x;
+            const int tok = last.tok0 + s * p.slot_tokens + my_tok, head = last.g * G + my_head;
             const float l_inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *out = p.out + ((size_t)(last.row0 + tok) * p.Hq + head) * 128;
             const int slot_row = last.slot * C::kUnitRows + s * kRows + row;
-            float4 *part = p.part_o + (((size_t)last.slot * (C::kUnitRows / 32) + s * 4 + wq) * 32) * 32 + lane;
+            float *part = p.part_o + (size_t)(slot_row & ~3) * 128 + 4 * (lane & 3);  // the first row of this group of four lanes
+            const int my_rows = min(max(last_r.z * G - (row & ~3), 0), 4);
             if (!last.whole && mine)  // an all-NaN row has l = NaN and no maximum: keep it from reading as empty
                 p.part_ml[slot_row] = make_float2(l != l ? 0.f : (m == -INFINITY ? m : m * qs), l);
             if (any) {
@@ -495,6 +633,10 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 if (!ok) return;
                 fence_after_sync();
             }
+            long long to[4];  // output rows of this group of four lanes, or -1
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                to[k] = __shfl_sync(0xffffffffu, mine ? ((long long)(last.row0 + tok) * p.Hq + head) * 128 : -1ll, (lane & ~3) + k);
             float bad = 0.f;  // stays 0 while every value of O is finite
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -508,8 +650,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) bad = fmaf(__uint_as_float(o[i]), 0.f, bad);
-                if (!mine) continue;
                 if (last.whole) {
+                    uint4 v[4];  // 16-byte chunks 4c .. 4c + 3 of this lane's row
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t h[4];
@@ -517,13 +659,24 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                         for (int k = 0; k < 4; ++k)
                             h[k] = h2_bits(__floats2half2_rn(__uint_as_float(o[8 * i + 2 * k]) * l_inv,
                                                              __uint_as_float(o[8 * i + 2 * k + 1]) * l_inv));
-                        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+                        v[i] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
+                    transpose4(v);  // now chunk 4c + (lane & 3) of the rows of this group of four lanes
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (to[k] >= 0) *reinterpret_cast<uint4 *>(p.out + to[k] + 32 * c + 8 * (lane & 3)) = v[k];
                 } else if (any) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        part[(8 * c + i) * 32] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    for (int i = 0; i < 2; ++i) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = make_uint4(o[16 * i + 4 * k], o[16 * i + 4 * k + 1], o[16 * i + 4 * k + 2], o[16 * i + 4 * k + 3]);
+                        transpose4(v);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < my_rows) *reinterpret_cast<uint4 *>(part + k * 128 + 32 * c + 16 * i) = v[k];
+                    }
                 }
             }
             if (any) {
@@ -552,43 +705,19 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     d[2] = float_to_half_bits(v.z * inv);
                     d[3] = float_to_half_bits(v.w * inv);
                 } else {
-                    p.part_o[(((size_t)last.slot * (C::kUnitRows / 32) + s * 4 + wq) * 32 + lane) * 32 + k] = v;
+                    reinterpret_cast<float4 *>(p.part_o)[((size_t)last.slot * C::kUnitRows + s * kRows + 32 * wq + k) * 32 + lane] = v;
                 }
             }
         };
 
         while (ok && walk.next(pc)) {
-            const int3 r = slot_tiles(p, G, pc, s);
-            if (r.y > r.x) {
-                // this row of Q, or zeros, into the swizzled tile; every MMA that read the last one is done, since its
-                // S has arrived
-                const int rr = pc.r0 + s * kRows + row;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(pc.row0 + rr / G) * p.q_stride +
-                                                                   (size_t)(pc.g * G + rr % G) * 128);
-                unsigned char *dst = gbase + s * kTileBytes + row * 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = row < r.z ? src[8 * h + c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(dst + h * kHalf + ((c ^ (row & 7)) << 4)) = v[c];
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[s]);
-            }
-            finish();
-            if (!ok) break;
-            last = pc;
-            last_r = r;
+            const int3 r = slot_tiles(p, pc, s);
             m = -INFINITY;
             l = 0.f;
-            if (r.y <= r.x) continue;
-            ++pieces;
+            pieces += r.y > r.x;
             int lo, hi;
             limits(pc, lo, hi);
-            if (row >= r.z) {  // no row: anything goes, nothing is stored
+            if (my_tok >= r.z) {  // no row: anything goes, nothing is stored
                 lo = 0;
                 hi = 0x7fffffff;
             }
@@ -611,10 +740,10 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 128; i += 8) {
-                    mx0 = fmaxf(mx0, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-                    mx1 = fmaxf(mx1, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
-                    mx2 = fmaxf(mx2, fmaxf(__uint_as_float(x[i + 4]), __uint_as_float(x[i + 5])));
-                    mx3 = fmaxf(mx3, fmaxf(__uint_as_float(x[i + 6]), __uint_as_float(x[i + 7])));
+                    mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+                    mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
+                    mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                 const bool up = mx > m + grow;
@@ -636,31 +765,43 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 const float mm = m == -INFINITY ? 0.f : -m * qs;
                 const float2 mm2 = make_float2(mm, mm), qs2 = make_float2(qs, qs);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                uint32_t h[16];
+                // P of 32 columns; kFma of every 16 pairs take their exponentials on the FMA units (see kFma)
+                auto weights = [&](int c) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t h[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
+                    for (int i = 0; i < 16; ++i) {
                         float2 u = ffma2(make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), qs2, mm2);
-                        float2 w =
-                            ffma2(make_float2(__uint_as_float(x[32 * c + 2 * i + 2]), __uint_as_float(x[32 * c + 2 * i + 3])), qs2, mm2);
-                        u = make_float2(ex2(u.x), ex2(u.y));
-                        w = make_float2(ex2(w.x), ex2(w.y));
-                        sum0 = fadd2(sum0, u);
-                        sum1 = fadd2(sum1, w);
+                        if ((i * kFma) % 16 + kFma > 15)
+                            u = ex2_fma(u);
+                        else
+                            u = make_float2(ex2(u.x), ex2(u.y));
+                        if (i & 1)
+                            sum1 = fadd2(sum1, u);
+                        else
+                            sum0 = fadd2(sum0, u);
                         h[i] = h2_bits(__floats2half2_rn(u.x, u.y));
-                        h[i + 1] = h2_bits(__floats2half2_rn(w.x, w.y));
                     }
-                    tmem_st16(tS + 16 * c, h);
-                }
-                tmem_wait_st();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[s]);
+                };
+                auto signal = [&](uint64_t *bar) {
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                weights(0);
+                tmem_st16(tS, h);
+                weights(1);
+                tmem_st16(tS + 16, h);
+                weights(2);
+                signal(&p_half[s]);  // the tensor cores start on the first half of P; its stores had a quarter's time to land
+                tmem_st16(tS + 32, h);
+                weights(3);
+                tmem_st16(tS + 48, h);
+                signal(&p_full[s]);
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             }
+            if (ok) finish(pc, r);
         }
-        if (ok) finish();
     }
     fence_before_sync();
     __syncthreads();
@@ -671,55 +812,63 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 }
 
 // The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
-// Grid (CTAs of the main kernel, row blocks of 32); lane = row, warp = 16 columns.
+// Grid (CTAs of the main kernel, row blocks of 32); one warp per row, lane = four columns. The weights of 32 parts are in the
+// lanes at once and the parts' rows are loaded eight at a time, so a row costs a few latencies whatever it was cut into.
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
     grid_dep_wait();
     const Cut c = p.cuts[blockIdx.x];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane;
-    if (!c.valid || (int)blockIdx.y * 32 >= c.rows || row >= c.rows) return;
-    const int G = p.Hq / p.Hkv, first = blockIdx.x;
-    auto slot = [&](int k) { return k < first ? 2 * k + 1 : 2 * k; };
-    float M = -INFINITY;
-    for (int k = first - 1; k <= c.last; ++k) M = fmaxf(M, p.part_ml[(size_t)slot(k) * unit_rows + row].x);
-    float L = 0.f;
-    float4 o[4];
+    if (!c.valid) return;
+    const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x, parts = c.last - first + 2;
+    const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
+    for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < (int)blockIdx.y * 32 + 32; row += 8) {
+        const int in_slot = (row % kRows) / G, tok = row / kRows * p.slot_tokens + in_slot;
+        if (in_slot >= p.slot_tokens || tok >= c.tokens) break;  // no row, nor any behind it in this block
+        float M = -INFINITY;
+        for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[(size_t)slot(k) * unit_rows + row].x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = first - 1; k <= c.last; ++k) {
-        const float2 ml = p.part_ml[(size_t)slot(k) * unit_rows + row];
-        if (ml.x == -INFINITY) continue;  // this part saw nothing: its O was not written
-        const float w = exp2f(ml.x - M);
-        L = fmaf(w, ml.y, L);
-        const float4 *src = p.part_o + (((size_t)slot(k) * (unit_rows / 32) + blockIdx.y) * 32 + 4 * warp) * 32 + lane;
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (k0 + lane < parts) ml = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row];
+            const bool some = ml.x > -INFINITY;  // a part that saw nothing has no O
+            const float w = some ? exp2f(ml.x - M) : 0.f;
+            L += warp_sum(w * ml.y);
+            const unsigned there = __ballot_sync(0xffffffffu, some);
+#pragma unroll 1
+            for (int k1 = 0; k1 < min(32, parts - k0); k1 += 8) {
+                float4 v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = src[i * 32];
-            o[i] = make_float4(fmaf(w, v.x, o[i].x), fmaf(w, v.y, o[i].y), fmaf(w, v.z, o[i].z), fmaf(w, v.w, o[i].w));
+                for (int k = 0; k < 8; ++k) {
+                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if ((there >> (k1 + k)) & 1)
+                        v[k] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row) * 32 + lane];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k1 + k);
+                    o = make_float4(fmaf(wk, v[k].x, o.x), fmaf(wk, v[k].y, o.y), fmaf(wk, v[k].z, o.z), fmaf(wk, v[k].w, o.w));
+                }
+            }
         }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint2 h;
+        h.x = h2_bits(__floats2half2_rn(o.x * inv, o.y * inv));
+        h.y = h2_bits(__floats2half2_rn(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + c.g * G + row % kRows - in_slot * G) * 128 + 4 * lane) = h;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int r = c.r0 + row;
-    uint16_t *out = p.out + ((size_t)(c.row0 + r / G) * p.Hq + c.g * G + r % G) * 128 + 16 * warp;
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[2 * i] = h2_bits(__floats2half2_rn(o[i].x * inv, o[i].y * inv));
-        h[2 * i + 1] = h2_bits(__floats2half2_rn(o[i].z * inv, o[i].w * inv));
-    }
-    reinterpret_cast<uint4 *>(out)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4 *>(out)[1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 // ------------------------------------------------------------------ host side
 
-// [pages][Hkv][P][128] fp16 as boxes of one page, one kv head and 64 dims.
-static int pool_map(CUtensorMap *m, const uint16_t *pool, int num_pages, int Hkv, int P) {
+// A tensor map of fp16 rows of 128 dims in boxes of 64: rows x y x z with the given strides in bytes and box sizes.
+static int row_map(CUtensorMap *m, const uint16_t *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                   const cuuint32_t (&box)[4]) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(I4_ECUDA, "i4_paged_gqa_chunk: cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[4] = {128, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
-    const cuuint64_t strides[3] = {256, 256ull * P, 256ull * P * Hkv};
-    const cuuint32_t box[4] = {64, (cuuint32_t)P, 1, 1}, step[4] = {1, 1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint16_t *>(pool), dims, strides, box, step,
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint16_t *>(base), dims, strides, box, step,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(I4_ECUDA, "i4_paged_gqa_chunk: tensor map encode failed (%d)", (int)r);
@@ -755,9 +904,9 @@ static int device_sms(int *sms) {
 }
 
 template <int NQ>
-static int launch_chunk(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkAttnParams &p, int sms, cudaStream_t stream) {
+static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkAttnParams &p, int sms, cudaStream_t stream) {
     const int grid = sms * Cfg<NQ>::kCtasPerSm;
-    chunk_attn_kernel<NQ><<<grid, Cfg<NQ>::kThreads, Cfg<NQ>::kSmem, stream>>>(tk, tv, p);
+    chunk_attn_kernel<NQ><<<grid, Cfg<NQ>::kThreads, Cfg<NQ>::kSmem, stream>>>(tq, tk, tv, p);
     int st = launch_check("i4_paged_gqa_chunk");
     if (st) return st;
     return cuda_check(launch(chunk_join_kernel, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, true, p,
@@ -817,17 +966,23 @@ extern "C" int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const u
     int sms = 0;
     int st = device_sms(&sms);
     if (st) return st;
-    CUtensorMap tk, tv;
-    if ((st = pool_map(&tk, k_pool, num_pages, Hkv, page_size))) return st;
-    if ((st = pool_map(&tv, v_pool, num_pages, Hkv, page_size))) return st;
+    const int G = Hq / Hkv;
+    CUtensorMap tq, tk, tv;
+    // q as [T][Hq][128] in boxes of one kv head's rows of a slot's tokens; the pools as [pages][Hkv][P][128] in boxes of a page
+    const cuuint64_t page = 256ull * page_size, tok = 2ull * (cuuint64_t)q_stride;
+    const cuuint64_t qd[4] = {128, (cuuint64_t)Hq, (cuuint64_t)T, 1}, qs[3] = {256, tok, tok * (cuuint64_t)T};
+    const cuuint64_t pd[4] = {128, (cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)num_pages}, ps[3] = {256, page, page * Hkv};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G), 1}, pb[4] = {64, (cuuint32_t)page_size, 1, 1};
+    if ((st = row_map(&tq, q, qd, qs, qb)) || (st = row_map(&tk, k_pool, pd, ps, pb)) || (st = row_map(&tv, v_pool, pd, ps, pb))) return st;
     ChunkAttnParams p = {q,   k_pool, v_pool, q_stride,  page_table,        q_start,   ctx_len, out,  T,
                          B,   Hq,     Hkv,    page_size, max_pages_per_seq, num_pages, window,  scale};
     char *w = reinterpret_cast<char *>(ws);
     p.cuts = reinterpret_cast<Cut *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + kWsMl);
-    p.part_o = reinterpret_cast<float4 *>(w + kWsO);
+    p.part_o = reinterpret_cast<float *>(w + kWsO);
+    p.slot_tokens = kRows / G;
     // one slot of 128 rows when every chunk fits it: the other warpgroup would idle
     const int longest = max_q > 0 && max_q < T ? max_q : T;
-    if (longest * (Hq / Hkv) <= kRows) return launch_chunk<1>(tk, tv, p, sms, (cudaStream_t)stream);
-    return launch_chunk<2>(tk, tv, p, sms, (cudaStream_t)stream);
+    if (longest <= p.slot_tokens) return launch_chunk<1>(tq, tk, tv, p, sms, (cudaStream_t)stream);
+    return launch_chunk<2>(tq, tk, tv, p, sms, (cudaStream_t)stream);
 }

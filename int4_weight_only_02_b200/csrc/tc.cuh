@@ -96,6 +96,14 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One thread of the warp. The compiler recognises this form and issues the tensor core's instructions in the branch with
+// uniform operands; under `lane == 0` it wraps each in a loop over the active lanes (about 140 cycles an instruction).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // D (tensor memory) += A (tensor memory, fp16 pairs, lane = row) * B (shared memory)
 __device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, int acc) {
     asm volatile(
