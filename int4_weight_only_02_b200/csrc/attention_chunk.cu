@@ -40,21 +40,20 @@ constexpr int kRows = 128;                         // rows of a slot: the MMA's 
 constexpr int kTile = 128;                         // positions of a K/V tile
 constexpr unsigned kHalf = kTile * 128;            // 64 of the 128 dims of a tile, 128 bytes per row
 constexpr unsigned kTileBytes = 2 * kHalf;         // 32 KB
+constexpr int kStep = kTile / 2;                   // positions that a slot's softmax takes at once
 constexpr int kMaxCtas = 2 * kNumSMs;
 constexpr float kGrow = 8.f;                       // powers of two that a row's maximum may run ahead of its m
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFma = 4;
 
 template <int NQ>
 struct Cfg {
-    // softmax warpgroups, an MMA warp each, the load warp; with NQ = 2 an idle warp fills the last warpgroup, which
-    // hands registers to the others (setmaxnreg): 256 * 208 + 128 * 88 = 384 * 168
-    static constexpr int kThreads = NQ == 2 ? 384 : 192;
+    static constexpr int kThreads = NQ == 2 ? 384 : 192;  // softmax warpgroups, an MMA warp each, the load warps
     static constexpr int kStages = NQ == 2 ? 5 : 2;
     static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
     static constexpr int kUnitRows = NQ * kRows;
-    static constexpr int kUnitCost = 1;  // what beginning and ending a unit costs, in tiles
+    static constexpr int kUnitCost = 2;  // what beginning and ending a unit costs, in tiles
     static constexpr int kMinCost = 2;   // tiles that are worth a CTA of their own
+    static constexpr int kWhole = 4;     // a unit of at most so many tiles is not cut: joining would take longer
     static constexpr unsigned kTmemCols = NQ * 256;  // S / P and O of every slot
     static constexpr unsigned kSmem = 1024 + (NQ + kStages) * kTileBytes;
 };
@@ -195,25 +194,42 @@ __device__ __forceinline__ int scan_block(int v, int &total, int *warp_sums) {
 // This CTA's stretch, and the cut at its beginning. scratch: 32 + 3 NT ints of shared memory.
 template <int NQ>
 __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *out, int *scratch) {
-    constexpr int NT = Cfg<NQ>::kThreads, V = Cfg<NQ>::kUnitCost;
+    using C = Cfg<NQ>;
+    constexpr int NT = C::kThreads, V = C::kUnitCost;
     const int tid = threadIdx.x, size = NQ * p.slot_tokens;
     int *sums = scratch, *first = scratch + 32, *tokens = first + NT, *pos = tokens + NT;  // units before sequence b0 + j; the sequence
-    if (tid == 0) *out = {0, 0, 0, 0, 0, 0, 0, 0};
-    long long W = 0, start = 0;
-    int n_ctas = 1, line = 0, target = 0, length = 0;
+    if (tid == 0) {
+        *out = {0, 0, 0, 0, 0, 0, 0, 0};
+        p.cuts[blockIdx.x].valid = 0;
+    }
+    long long W = 0, start = 0, end = 0;
+    int n_ctas = 1, line = 0;
     int cost = 0, at = 0, j = 0, i = 0;  // this thread's unit: unit i of sequence b0 + j
+    // The unit that a border of the stretch lies in, for the thread that has it: a short unit goes whole to the CTA behind.
+    auto offset = [&](long long border) {
+        const int off = (int)(border % line) - at;
+        return off < 0 || off >= cost ? -1 : (cost <= V + C::kWhole ? 0 : off);
+    };
     auto place = [&](int b0) {
-        if (cost == 0 || target < at || target >= at + cost) return;
-        const int g = (int)(start / line), off = target - at;
-        const int2 seq = chunk_rows(p.q_start, b0 + j, p.T);
-        *out = {g, b0 + j, i, off, length, seq.y, pos[j], seq.x};
-        Cut cut = {0, 0, 0, 0, 0};
-        const long long unit = start - off;  // where the unit begins
-        if (off > V && W * (blockIdx.x - 1) / n_ctas <= unit + V) {
-            // the first cut of this unit: its parts end in the CTA that holds its last tile
-            cut = {1, (int)(((unit + cost) * n_ctas - 1) / W), min(seq.y - i * size, size), seq.x + i * size, g};
+        const int off = offset(start);
+        if (off >= 0) {
+            const int2 seq = chunk_rows(p.q_start, b0 + j, p.T);
+            const long long unit = start - (start % line - at);  // where the unit begins
+            out->g = (int)(start / line);
+            out->b = b0 + j;
+            out->i = i;
+            out->off = off;
+            out->n = seq.y;
+            out->pos0 = pos[j];
+            out->row0 = seq.x;
+            atomicSub(&out->left, (int)(unit + off - start));
+            if (off > V && W * (blockIdx.x - 1) / n_ctas <= unit + V)
+                // the first cut of this unit: its parts end in the CTA that holds its last tile
+                p.cuts[blockIdx.x] = {1, (int)(((unit + cost) * n_ctas - 1) / W), min(seq.y - i * size, size), seq.x + i * size,
+                                      (int)(start / line)};
         }
-        p.cuts[blockIdx.x] = cut;
+        const int off_end = end < W ? offset(end) : -1;
+        if (off_end >= 0) atomicAdd(&out->left, off_end - (int)(end % line - at));
     };
     for (int pass = 0; pass < 2; ++pass) {  // the first measures the line, the second finds the place in it
         int run = 0, trips = 0;
@@ -256,14 +272,12 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
         if (pass == 0) {
             line = run;
             W = (long long)line * p.Hkv;
-            n_ctas = (int)min((long long)gridDim.x, max((W + Cfg<NQ>::kMinCost - 1) / Cfg<NQ>::kMinCost, 1ll));
+            n_ctas = (int)min((long long)gridDim.x, max((W + C::kMinCost - 1) / C::kMinCost, 1ll));
             start = W * blockIdx.x / n_ctas;
-            length = (int)(W * (blockIdx.x + 1) / n_ctas - start);
-            if ((int)blockIdx.x >= n_ctas || length <= 0) {
-                if (tid == 0) p.cuts[blockIdx.x].valid = 0;
-                break;
-            }
-            target = (int)(start % line);
+            end = W * (blockIdx.x + 1) / n_ctas;
+            if ((int)blockIdx.x >= n_ctas || start >= end) break;
+            if (tid == 0) out->left = (int)(end - start);
+            __syncthreads();
             if (trips == 1 && p.B <= NT) {  // every unit is still in its thread's hands
                 place(0);
                 break;
@@ -279,22 +293,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// 2^x for two values on the FMA units: x = n + f with n the nearest integer (Cody and Waite's reduction, by adding
-// and taking away 1.5 * 2^23), a polynomial for 2^f on [-1/2, 1/2] (degree 4, least relative maximum error, own fit:
-// 2.7e-6 in fp32), and n added to the exponent. x below -126 gives less than 2^-125, which is zero in fp16.
-__device__ __forceinline__ float2 ex2_fma(float2 x) {
-    const float2 big = make_float2(12582912.f, 12582912.f), none = make_float2(-1.f, -1.f);
-    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-    const float2 t = fadd2(x, big);
-    const float2 f = fadd2(x, ffma2(t, none, big));
-    float2 y = ffma2(f, make_float2(0.00957010221f, 0.00957010221f), make_float2(0.0559178703f, 0.0559178703f));
-    y = ffma2(y, f, make_float2(0.240247443f, 0.240247443f));
-    y = ffma2(y, f, make_float2(0.693121791f, 0.693121791f));
-    y = ffma2(y, f, make_float2(0.999999285f, 0.999999285f));
-    return make_float2(__uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -374,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     using C = Cfg<NQ>;
     constexpr int S = C::kStages, kMmaWarp = NQ * 4, kLoadWarp = kMmaWarp + NQ;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], q_free[NQ], s_full[NQ], p_half[NQ], p_full[NQ], o_full[NQ], o_free[NQ], turn[NQ], all_done;
+    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], q_free[NQ], s_full[NQ][2], p_full[NQ][2], pv_done[NQ][2], o_free[NQ], all_done;
     __shared__ uint32_t tmem_base;
     __shared__ Stretch stretch;
     __shared__ int stop_flag;
@@ -394,12 +392,12 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
         for (int s = 0; s < NQ; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_free[s], 1);
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_half[s], 4);
-            mbar_init(&p_full[s], 4);
-            mbar_init(&o_full[s], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&s_full[s][h], 1);
+                mbar_init(&p_full[s][h], 4);
+                mbar_init(&pv_done[s][h], 1);
+            }
             mbar_init(&o_free[s], 4);
-            mbar_init(&turn[s], 1);
         }
         mbar_init(&all_done, NQ);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -424,7 +422,6 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     if (stretch.left <= 0) {
         // no work: straight to the end
     } else if (warp >= kMmaWarp) {
-    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // The rows of Q of one slot's piece: tokens behind the sequence's are another's, or zeros behind the last row; nothing
     // that comes of them is stored.
     auto load_q = [&](const Piece &c, int s) {
@@ -503,11 +500,11 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     } else if (warp < kMmaWarp + NQ) {
         // ---------------- S = Q K^T and O += P V of slot s. One warp per slot: a tile takes a warp some 150 instructions that
         // nothing else on its scheduler shares, and both slots' in one warp took longer than the tensor cores' own work
-        constexpr uint32_t idesc_qk = idesc_f16(kRows, kTile), idesc_pv = idesc_f16(kRows, 128) | kIdescBMajorMN;
+        constexpr uint32_t idesc_qk = idesc_f16(kRows, kStep), idesc_pv = idesc_f16(kRows, 128) | kIdescBMajorMN;
         const int s = (int)uniform((uint32_t)(warp - kMmaWarp));
-        const uint32_t tP = tmem + 128 * s, tO = tmem + 128 * (NQ + s);
+        const uint32_t tS = tmem + 128 * s, tO = tmem + 128 * (NQ + s);
         const uint64_t qd = desc_sw128(base + s * kTileBytes), kd0 = desc_sw128(ring), vd0 = desc_sw128_mn(ring, kHalf);
-        unsigned it = 0, uses = 0, steps = 0, turns = 0;  // ring entries, pieces, tiles and turns so far
+        unsigned it = 0, uses = 0, steps = 0;  // ring entries, pieces and tiles so far
         bool ok = true;
         while (ok && walk.next(pc)) {
             const int3 r = slot_tiles(p, pc, s);
@@ -517,6 +514,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 // entries it - 1: V of tile j, it: K of tile j + 1
                 const unsigned sv = (it - 1) % S, sk = it % S;
                 const bool has_v = j >= pc.t0, has_k = j + 1 < pc.t1;
+                const bool pv = j >= r.x && j < r.y, qk = j + 1 >= r.x && j + 1 < r.y;
                 if (has_v) {
                     ok = wait_or_stop(&kv_full[sv], ((it - 1) / S) & 1, stop);
                     const int t = j * kTile;
@@ -533,65 +531,44 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     __syncwarp();
                 }
                 if (ok && has_k) ok = wait_or_stop(&kv_full[sk], (it / S) & 1, stop);
-                const bool pv = j >= r.x && j < r.y;
-                if (ok && pv) ok = wait_or_stop(&p_half[s], steps & 1, stop);
-                if (NQ == 2 && ok && (s == 1 || turns > 0)) ok = wait_or_stop(&turn[s], (turns - (s == 0)) & 1, stop);
-                ++turns;
-                if (has_v) {
-                    if (pv) {
-                        if (ok && j == r.x) {
-                            if (uses > 0) ok = wait_or_stop(&o_free[s], (uses - 1) & 1, stop);
-                            ++uses;
-                        }
-                        const uint64_t vd = vd0 + uniform(sv) * (kTileBytes >> 4);
-                        const int more = j > r.x;
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                        fence_after_sync();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < kTile / 32; ++kk)
-                                umma_f16_ta(tO, tP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1 : more);
-                        }
-                        __syncwarp();
-                        ok = wait_or_stop(&p_full[s], steps & 1, stop);
-                        ++steps;
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                        fence_after_sync();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = kTile / 32; kk < kTile / 16; ++kk)
-                                umma_f16_ta(tO, tP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, 1);
-                            umma_commit(&kv_empty[sv]);
-                            if (j + 1 == r.y) umma_commit(&o_full[s]);
-                        }
-                        __syncwarp();
-                    } else {
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                        if (elect_one()) umma_commit(&kv_empty[sv]);
-                        __syncwarp();
-                    }
+                if (ok && qk && j + 1 == r.x) ok = wait_or_stop(&q_full[s], uses & 1, stop);
+                if (ok && pv && j == r.x) {
+                    if (uses > 0) ok = wait_or_stop(&o_free[s], (uses - 1) & 1, stop);
+                    ++uses;
                 }
-                if (has_k) {
-                    const bool mine = j + 1 >= r.x && j + 1 < r.y;
-                    if (ok && mine && j + 1 == r.x) ok = wait_or_stop(&q_full[s], uses & 1, stop);
-                    const uint64_t kd = kd0 + uniform(sk) * (kTileBytes >> 4);
+                const uint64_t vd = vd0 + uniform(sv) * (kTileBytes >> 4), kd = kd0 + uniform(sk) * (kTileBytes >> 4);
+                const int more = j > r.x;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {  // the halves of the tile: P V of one, then the next tile's S over it
+                    if (ok && pv) ok = wait_or_stop(&p_full[s][h], steps & 1, stop);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     fence_after_sync();
                     if (elect_one()) {
-                        if (mine) {
+                        if (pv) {
+#pragma unroll
+                            for (int kk = 0; kk < kStep / 16; ++kk)
+                                umma_f16_ta(tO, tS + kStep * h + 8 * kk, vd + (h * (kStep / 16) + kk) * (2048 >> 4), idesc_pv,
+                                            kk > 0 ? 1 : (more | h));
+                            umma_commit(&pv_done[s][h]);
+                        }
+                        if (qk) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
                                 const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                                umma_f16(tP, qd + o, kd + o, idesc_qk, kk > 0 ? 1 : 0);
+                                umma_f16(tS + kStep * h, qd + o, kd + o + h * (kStep * 128 >> 4), idesc_qk, kk > 0 ? 1 : 0);
                             }
-                            umma_commit(&s_full[s]);
-                            if (j + 2 == r.y) umma_commit(&q_free[s]);
+                            umma_commit(&s_full[s][h]);
                         }
-                        umma_commit(&kv_empty[sk]);
+                        if (h == 1) {
+                            if (has_v) umma_commit(&kv_empty[sv]);
+                            if (has_k) umma_commit(&kv_empty[sk]);
+                            if (qk && j + 2 == r.y) umma_commit(&q_free[s]);
+                        }
                     }
                     __syncwarp();
                 }
-                if (NQ == 2 && lane == 0) mbar_arrive(&turn[s ^ 1]);
+                steps += pv;
+                if (!__all_sync(0xffffffffu, ok)) break;
             }
             ok = __all_sync(0xffffffffu, ok);
             it -= 2;
@@ -603,13 +580,12 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     }
     } else {
         // ---------------- softmax of slot s: thread = row
-        if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int s = warp >> 2, wq = warp & 3, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t tS = tmem + 128 * s + lanes, tO = tmem + 128 * (NQ + s) + lanes;
         const int my_tok = row / G, my_head = row - my_tok * G;  // within the slot and the kv head
         const float qs = p.scale * kLog2e, grow = fminf(kGrow / qs, 1e30f);
-        unsigned tiles = 0, pieces = 0;
+        unsigned tiles = 0;  // so far; each was two halves of P
         bool ok = true;
 
         float m = -INFINITY, l = 0.f;
@@ -629,7 +605,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
             if (!last.whole && mine)  // an all-NaN row has l = NaN and no maximum: keep it from reading as empty
                 p.part_ml[slot_row] = make_float2(l != l ? 0.f : (m == -INFINITY ? m : m * qs), l);
             if (any) {
-                ok = __all_sync(0xffffffffu, wait_or_stop(&o_full[s], (pieces - 1) & 1, stop));
+                ok = wait_or_stop(&pv_done[s][0], (tiles - 1) & 1, stop) && wait_or_stop(&pv_done[s][1], (tiles - 1) & 1, stop);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 fence_after_sync();
             }
@@ -714,7 +691,6 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
             const int3 r = slot_tiles(p, pc, s);
             m = -INFINITY;
             l = 0.f;
-            pieces += r.y > r.x;
             int lo, hi;
             limits(pc, lo, hi);
             if (my_tok >= r.z) {  // no row: anything goes, nothing is stored
@@ -722,24 +698,25 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 hi = 0x7fffffff;
             }
 #pragma unroll 1
-            for (int t = r.x; t < r.y; ++t, ++tiles) {
-                ok = __all_sync(0xffffffffu, wait_or_stop(&s_full[s], tiles & 1, stop));
+            for (int u = 2 * r.x; u < 2 * r.y; ++u) {  // halves of tiles
+                const int h = u & 1;
+                ok = __all_sync(0xffffffffu, wait_or_stop(&s_full[s][h], tiles & 1, stop));
                 if (!ok) break;
                 fence_after_sync();
-                uint32_t x[128];
+                uint32_t x[kStep];
+                tmem_ld32(tS + kStep * h, x);
+                tmem_ld32(tS + kStep * h + 32, x + 32);
+                tmem_wait_ld32(x);
+                tmem_wait_ld32(x + 32);
+                const int a = lo - u * kStep, e = hi - u * kStep;  // the row sees [a, e) of these positions
+                if (__any_sync(0xffffffffu, a > 0 || e < kStep)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_wait_ld32(x + 32 * c);
-                const int a = lo - t * kTile, e = hi - t * kTile;  // the row sees the tile's [a, e)
-                if (__any_sync(0xffffffffu, a > 0 || e < kTile)) {
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
+                    for (int i = 0; i < kStep; ++i)
                         if (i < a || i >= e) x[i] = 0xff800000u;  // -inf
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 128; i += 8) {
+                for (int i = 0; i < kStep; i += 8) {
                     mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
                     mx2 = max3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
@@ -747,58 +724,49 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                 const bool up = mx > m + grow;
-                const float m_old = m;
-                if (up) m = mx;
-                const float alpha = up ? ex2((m_old - m) * qs) : 1.f;  // 0 for a row that had seen nothing
-                l *= alpha;
-                if (t > r.x && __any_sync(0xffffffffu, up)) {  // O is still: P V of the tile before precedes this S
+                if (__any_sync(0xffffffffu, up)) {
+                    const float alpha = up ? ex2((m - mx) * qs) : 1.f;  // 0 for a row that had seen nothing
+                    if (up) m = mx;
+                    l *= alpha;
+                    if (u > 2 * r.x) {  // O holds still once P V of the half before has ended
+                        ok = __all_sync(0xffffffffu, wait_or_stop(&pv_done[s][h ^ 1], (tiles - (h ^ 1)) & 1, stop));
+                        if (!ok) break;
+                        fence_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32 * c, o);
-                        tmem_wait_ld32(o);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32 * c, o);
+                            tmem_wait_ld32(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + 32 * c, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + 32 * c, o);
+                        }
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : -m * qs;
                 const float2 mm2 = make_float2(mm, mm), qs2 = make_float2(qs, qs);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-                uint32_t h[16];
-                // P of 32 columns; kFma of every 16 pairs take their exponentials on the FMA units (see kFma)
-                auto weights = [&](int c) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 u = ffma2(make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), qs2, mm2);
-                        if ((i * kFma) % 16 + kFma > 15)
-                            u = ex2_fma(u);
-                        else
-                            u = make_float2(ex2(u.x), ex2(u.y));
+                        float2 v = ffma2(make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), qs2, mm2);
+                        v = make_float2(ex2(v.x), ex2(v.y));
                         if (i & 1)
-                            sum1 = fadd2(sum1, u);
+                            sum1 = fadd2(sum1, v);
                         else
-                            sum0 = fadd2(sum0, u);
-                        h[i] = h2_bits(__floats2half2_rn(u.x, u.y));
+                            sum0 = fadd2(sum0, v);
+                        w[i] = h2_bits(__floats2half2_rn(v.x, v.y));
                     }
-                };
-                auto signal = [&](uint64_t *bar) {
-                    tmem_wait_st();
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
-                };
-                weights(0);
-                tmem_st16(tS, h);
-                weights(1);
-                tmem_st16(tS + 16, h);
-                weights(2);
-                signal(&p_half[s]);  // the tensor cores start on the first half of P; its stores had a quarter's time to land
-                tmem_st16(tS + 32, h);
-                weights(3);
-                tmem_st16(tS + 48, h);
-                signal(&p_full[s]);
+                    tmem_st16(tS + kStep * h + 16 * c, w);
+                }
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[s][h]);
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                tiles += h;
             }
             if (ok) finish(pc, r);
         }
@@ -812,50 +780,77 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 }
 
 // The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
-// Grid (CTAs of the main kernel, row blocks of 32); one warp per row, lane = four columns. The weights of 32 parts are in the
-// lanes at once and the parts' rows are loaded eight at a time, so a row costs a few latencies whatever it was cut into.
+// Grid (CTAs of the main kernel, row blocks of 32); a warp has four rows, lane = four columns. The weights of 32 parts are in
+// the lanes at once and sixteen loads are in flight, so the kernel costs a few latencies (it is bound by nothing else).
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
     grid_dep_wait();
     const Cut c = p.cuts[blockIdx.x];
     if (!c.valid) return;
     const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x, parts = c.last - first + 2;
     const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
-    for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < (int)blockIdx.y * 32 + 32; row += 8) {
-        const int in_slot = (row % kRows) / G, tok = row / kRows * p.slot_tokens + in_slot;
-        if (in_slot >= p.slot_tokens || tok >= c.tokens) break;  // no row, nor any behind it in this block
-        float M = -INFINITY;
-        for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[(size_t)slot(k) * unit_rows + row].x);
+    constexpr int R = 4;  // rows of a warp, all in flight together
+    const int row0 = blockIdx.y * 32 + R * (threadIdx.x >> 5);
+    bool in[R];
+    float M[R], L[R];
+    float4 o[R];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < parts; k0 += 32) {
+    for (int i = 0; i < R; ++i) {
+        const int in_slot = (row0 + i) % kRows / G;
+        in[i] = in_slot < p.slot_tokens && (row0 + i) / kRows * p.slot_tokens + in_slot < c.tokens;
+        M[i] = -INFINITY;
+        L[i] = 0.f;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (!in[0]) return;  // rows of a slot without tokens are its last
+    for (int k = lane; k < parts; k += 32)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (in[i]) M[i] = fmaxf(M[i], p.part_ml[(size_t)slot(k) * unit_rows + row0 + i].x);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float w[R];
+        unsigned there[R];  // parts that saw something: the others have no O
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
             float2 ml = make_float2(-INFINITY, 0.f);
-            if (k0 + lane < parts) ml = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row];
-            const bool some = ml.x > -INFINITY;  // a part that saw nothing has no O
-            const float w = some ? exp2f(ml.x - M) : 0.f;
-            L += warp_sum(w * ml.y);
-            const unsigned there = __ballot_sync(0xffffffffu, some);
-#pragma unroll 1
-            for (int k1 = 0; k1 < min(32, parts - k0); k1 += 8) {
-                float4 v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if ((there >> (k1 + k)) & 1)
-                        v[k] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row) * 32 + lane];
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k1 + k);
-                    o = make_float4(fmaf(wk, v[k].x, o.x), fmaf(wk, v[k].y, o.y), fmaf(wk, v[k].z, o.z), fmaf(wk, v[k].w, o.w));
-                }
-            }
+            if (in[i] && k0 + lane < parts) ml = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row0 + i];
+            w[i] = ml.x > -INFINITY ? exp2f(ml.x - M[i]) : 0.f;
+            L[i] += warp_sum(w[i] * ml.y);
+            there[i] = __ballot_sync(0xffffffffu, ml.x > -INFINITY);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int n = min(32, parts - k0);
+#pragma unroll 1
+        for (int k1 = 0; k1 < n; k1 += 4) {
+            float4 v[4][R];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if ((there[i] >> (k1 + k)) & 1)
+                        v[k][i] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row0 + i) * 32 + lane];
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float wk = __shfl_sync(0xffffffffu, w[i], k1 + k);
+                    o[i] = make_float4(fmaf(wk, v[k][i].x, o[i].x), fmaf(wk, v[k][i].y, o[i].y), fmaf(wk, v[k][i].z, o[i].z),
+                                       fmaf(wk, v[k][i].w, o[i].w));
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (!in[i]) continue;
+        const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+        const int row = row0 + i, in_slot = row % kRows / G, tok = row / kRows * p.slot_tokens + in_slot;
         uint2 h;
-        h.x = h2_bits(__floats2half2_rn(o.x * inv, o.y * inv));
-        h.y = h2_bits(__floats2half2_rn(o.z * inv, o.w * inv));
+        h.x = h2_bits(__floats2half2_rn(o[i].x * inv, o[i].y * inv));
+        h.y = h2_bits(__floats2half2_rn(o[i].z * inv, o[i].w * inv));
         *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + c.g * G + row % kRows - in_slot * G) * 128 + 4 * lane) = h;
     }
 }
