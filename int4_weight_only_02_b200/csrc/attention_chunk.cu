@@ -781,12 +781,13 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 
 // The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
 // Grid (CTAs of the main kernel, row blocks of 32); a warp has four rows, lane = four columns. The weights of 32 parts are in
-// the lanes at once and sixteen loads are in flight, so the kernel costs a few latencies (it is bound by nothing else).
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
+// the lanes at once and eight loads are in flight, so the kernel costs a few latencies (it is bound by nothing else).
+__global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
+    const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x;
     grid_dep_wait();
-    const Cut c = p.cuts[blockIdx.x];
+    const Cut c = p.cuts[first];
     if (!c.valid) return;
-    const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x, parts = c.last - first + 2;
+    const int parts = c.last - first + 2;
     const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
     constexpr int R = 4;  // rows of a warp, all in flight together
     const int row0 = blockIdx.y * 32 + R * (threadIdx.x >> 5);
@@ -802,31 +803,39 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (!in[0]) return;  // rows of a slot without tokens are its last
-    for (int k = lane; k < parts; k += 32)
+    float2 ml[R];  // of part `lane`; the parts behind 32 are read again below
+    auto load_ml = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (in[i]) M[i] = fmaxf(M[i], p.part_ml[(size_t)slot(k) * unit_rows + row0 + i].x);
+        for (int i = 0; i < R; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (in[i] && k0 + lane < parts) ml[i] = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row0 + i];
+        }
+    };
+    for (int k0 = (parts - 1) & ~31; k0 >= 0; k0 -= 32) {
+        load_ml(k0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) M[i] = fmaxf(M[i], ml[i].x);
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
     for (int k0 = 0; k0 < parts; k0 += 32) {
+        if (k0 > 0) load_ml(k0);
         float w[R];
         unsigned there[R];  // parts that saw something: the others have no O
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (in[i] && k0 + lane < parts) ml = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row0 + i];
-            w[i] = ml.x > -INFINITY ? exp2f(ml.x - M[i]) : 0.f;
-            L[i] += warp_sum(w[i] * ml.y);
-            there[i] = __ballot_sync(0xffffffffu, ml.x > -INFINITY);
+            w[i] = ml[i].x > -INFINITY ? exp2f(ml[i].x - M[i]) : 0.f;
+            L[i] += warp_sum(w[i] * ml[i].y);
+            there[i] = __ballot_sync(0xffffffffu, ml[i].x > -INFINITY);
         }
         const int n = min(32, parts - k0);
 #pragma unroll 1
-        for (int k1 = 0; k1 < n; k1 += 4) {
-            float4 v[4][R];
+        for (int k1 = 0; k1 < n; k1 += 2) {
+            float4 v[2][R];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -834,7 +843,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
                         v[k][i] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row0 + i) * 32 + lane];
                 }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const float wk = __shfl_sync(0xffffffffu, w[i], k1 + k);
