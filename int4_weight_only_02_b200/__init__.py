@@ -326,20 +326,30 @@ def _refuse(name: str, what: str):
     raise I4Error(I4_EINVAL, f"{name}: {what}")
 
 
-def _tensors(name: str, *groups):
+def _tensors(name: str, *groups) -> int:
     """Refuses tensors that the call could not follow: every (tensor, dtype, dims) has that type and number of
-    dimensions, is contiguous and lies on the current CUDA device (whose current stream the call uses)."""
+    dimensions, is contiguous and lies on the current CUDA device (whose current stream the call uses). Returns the
+    device's index. The calls below take microseconds on the GPU, so what is asked of each tensor is kept cheap."""
     import torch
     for t, dtype, dims in groups:
         if t.dtype is not dtype or t.dim() != dims or not t.is_contiguous():
             _refuse(name, f"a contiguous {dtype} tensor of {dims} dimensions is needed, got {t.dtype} {tuple(t.shape)}")
-    dev = groups[0][0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        _refuse(name, f"tensors on the current CUDA device are needed, got {dev}")
+    dev = groups[0][0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(name, f"tensors on the current CUDA device are needed, got {groups[0][0].device}")
     for t, _, _ in groups:
-        if t.device != dev:
-            _refuse(name, f"tensors on {dev} and {t.device}")
+        if t.get_device() != dev:
+            _refuse(name, f"tensors on cuda:{dev} and {t.device}")
     return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """cudaStream_t of `stream`, or of device dev's current stream (without the stream object that
+    torch.cuda.current_stream() makes)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
@@ -370,22 +380,24 @@ def rope_append_chunk(qkv, q_start, ctx_len, cs, Hq: int, Hkv: int, k_pool, v_po
     f16, i32 = torch.float16, torch.int32
     if qkv.dim() != 2 or qkv.dtype is not f16 or (qkv.stride(1) != 1 and qkv.shape[1] > 1):
         _refuse(name, "qkv [T][(Hq+2Hkv)*128] fp16 with adjacent columns is needed")
-    T, B = qkv.shape[0], page_table.shape[0]
+    T, width = qkv.shape
+    B, max_pages = page_table.shape
     if q_out is None:
         q_out = torch.zeros((T, Hq, 128), device=qkv.device, dtype=f16)
     dev = _tensors(name, (q_start, i32, 1), (ctx_len, i32, 1), (cs, torch.float32, 3), (k_pool, f16, 4), (v_pool, f16, 4),
                    (page_table, i32, 2), (q_out, f16, 3))
-    num_pages, hkv, P, D = k_pool.shape
-    if (qkv.device != dev or qkv.shape[1] != (Hq + 2 * Hkv) * D or hkv != Hkv or v_pool.shape != k_pool.shape
-            or q_out.shape != (T, Hq, D) or q_start.numel() != B + 1 or ctx_len.numel() != B or cs.shape[2] != 2):
+    num_pages, hkv, P, D = shape = k_pool.shape
+    max_pos, half, two = cs.shape
+    if (qkv.get_device() != dev or width != (Hq + 2 * Hkv) * D or hkv != Hkv or v_pool.shape != shape
+            or q_out.shape != (T, Hq, D) or q_start.numel() != B + 1 or ctx_len.numel() != B or two != 2):
         _refuse(name, f"shapes do not match: qkv {tuple(qkv.shape)}, pools {tuple(k_pool.shape)} {tuple(v_pool.shape)}, "
                       f"q_out {tuple(q_out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
     if T == 0 or B == 0:
         return q_out
-    _check(lib().i4_rope_append_chunk(_p(qkv), qkv.stride(0), _p(q_start), _p(ctx_len), _p(cs), cs.shape[0],
-                                      cs.shape[1] * 2, int(interleaved), T, B, Hq, Hkv, D, _p(q_out), _p(k_pool),
-                                      _p(v_pool), _p(page_table), P, page_table.shape[1], num_pages, _stream(stream)),
-           name)
+    _check(lib().i4_rope_append_chunk(qkv.data_ptr(), qkv.stride(0) if T > 1 else width, q_start.data_ptr(), ctx_len.data_ptr(),
+                                      cs.data_ptr(), max_pos, half * 2, int(interleaved), T, B, Hq, Hkv, D,
+                                      q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), P,
+                                      max_pages, num_pages, _raw_stream(stream, dev)), name)
     return q_out
 
 
@@ -404,52 +416,62 @@ def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, w
     f16, i32 = torch.float16, torch.int32
     if q.dim() != 3 or q.dtype is not f16 or q.stride(2) != 1 or (q.stride(1) != q.shape[2] and q.shape[1] > 1):
         _refuse(name, "q [T][Hq][128] fp16 with adjacent heads is needed")
-    T, Hq, D = q.shape
-    B = page_table.shape[0]
+    T, Hq, D = shape = q.shape
+    B, max_pages = page_table.shape
     if out is None:
         out = torch.zeros((T, Hq, D), device=q.device, dtype=f16)
+    if ws is None:
+        ws = torch.empty(paged_gqa_chunk_ws_bytes(), device=q.device, dtype=torch.uint8)
     dev = _tensors(name, (k_pool, f16, 4), (v_pool, f16, 4), (page_table, i32, 2), (q_start, i32, 1), (ctx_len, i32, 1),
-                   (out, f16, 3))
-    num_pages, Hkv, P, dk = k_pool.shape
-    if (q.device != dev or dk != D or v_pool.shape != k_pool.shape or out.shape != q.shape or q_start.numel() != B + 1
+                   (out, f16, 3), (ws, torch.uint8, 1))
+    num_pages, Hkv, P, dk = pool = k_pool.shape
+    if (q.get_device() != dev or dk != D or v_pool.shape != pool or out.shape != shape or q_start.numel() != B + 1
             or ctx_len.numel() != B):
         _refuse(name, f"shapes do not match: q {tuple(q.shape)}, pools {tuple(k_pool.shape)} {tuple(v_pool.shape)}, out "
                       f"{tuple(out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
     if T == 0 or B == 0:
         return out
-    if ws is None:
-        ws = torch.empty(paged_gqa_chunk_ws_bytes(), device=dev, dtype=torch.uint8)
-    _check(lib().i4_paged_gqa_chunk(_p(q), q.stride(0) if T > 1 else Hq * D, _p(k_pool), _p(v_pool), _p(page_table),
-                                    _p(q_start), _p(ctx_len), _p(out), T, B, Hq, Hkv, D, P, page_table.shape[1], num_pages,
-                                    int(window), int(max_q), 1.0 / D ** 0.5 if scale is None else float(scale), _p(ws),
-                                    ws.numel() * ws.element_size(), _stream(stream)), name)
+    _check(lib().i4_paged_gqa_chunk(q.data_ptr(), q.stride(0) if T > 1 else Hq * D, k_pool.data_ptr(), v_pool.data_ptr(),
+                                    page_table.data_ptr(), q_start.data_ptr(), ctx_len.data_ptr(), out.data_ptr(), T, B, Hq,
+                                    Hkv, D, P, max_pages, num_pages, int(window), int(max_q),
+                                    D ** -0.5 if scale is None else float(scale), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream, dev)), name)
     return out
 
 
 def _pool_array(name: str, pools):
-    """(host array of the pools' addresses, shape of a pool) of a sequence of equal fp16 pools."""
+    """(host array of the pools' addresses, shape of a pool) of a sequence of equal pools of 16-bit values."""
     import torch
+    T = torch.Tensor
     shape = pools[0].shape if len(pools) else ()
     if len(shape) != 4:
         _refuse(name, "pools [num_pages][Hkv][page_size][D] are needed")
-    dev = pools[0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        _refuse(name, f"pools on the current CUDA device are needed, got {dev}")
-    for t in pools:
-        if t.shape != shape or t.element_size() != 2 or not t.is_contiguous() or t.device != dev:
-            _refuse(name, "pools of one shape, two bytes a value, contiguous and on one device are needed")
-    return (_vp * len(pools))(*[t.data_ptr() for t in pools]), shape
+    dev = pools[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(name, f"pools on the current CUDA device are needed, got {pools[0].device}")
+    if (set(map(T.size, pools)) != {shape} or set(map(T.element_size, pools)) != {2} or not all(map(T.is_contiguous, pools))
+            or set(map(T.get_device, pools)) != {dev}):
+        _refuse(name, "pools of one shape, two bytes a value, contiguous and on one device are needed")
+    return (_vp * len(pools))(*map(T.data_ptr, pools)), shape
 
 
-def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, *lists):
+def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, ws, *lists):
+    """(the cache's descriptor, its device)."""
     import torch
     i32 = torch.int32
-    _tensors(name, (page_table, i32, 2), (ctx_len, i32, 1), (refs, i32, 1), *[(t, i32, 1) for t in lists])
-    if ctx_len.numel() != page_table.shape[0] or any(t.numel() != lists[0].numel() for t in lists):
-        _refuse(name, f"shapes do not match: page_table {tuple(page_table.shape)}, ctx_len {tuple(ctx_len.shape)}, lists "
-                      f"{[t.numel() for t in lists]}")
-    return KvCacheDesc(page_table.data_ptr(), ctx_len.data_ptr(), refs.data_ptr(), page_table.shape[0],
-                       page_table.shape[1], int(page_size), refs.numel())
+    groups = [(page_table, i32, 2), (ctx_len, i32, 1), (refs, i32, 1)]
+    if ws is not None:
+        groups.append((ws, torch.uint8, 1))
+    n = lists[0].numel()
+    for t in lists:
+        groups.append((t, i32, 1))
+        if t.numel() != n:
+            _refuse(name, f"lists of different lengths: {[t.numel() for t in lists]}")
+    dev = _tensors(name, *groups)
+    S, width = page_table.shape
+    if ctx_len.numel() != S:
+        _refuse(name, f"shapes do not match: page_table {tuple(page_table.shape)}, ctx_len {tuple(ctx_len.shape)}")
+    return KvCacheDesc(page_table.data_ptr(), ctx_len.data_ptr(), refs.data_ptr(), S, width, page_size, refs.numel()), dev
 
 
 def kv_pages_ws_bytes(num_pages: int, n_seqs: int) -> int:
@@ -468,11 +490,11 @@ def kv_pages_copy(pools, src, dst, stream=None):
     """Page src[i] -> dst[i] in every pool (device int32 lists; no page may be both source and target)."""
     import torch
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_copy", pools)
-    _tensors("kv_pages_copy", (src, torch.int32, 1), (dst, torch.int32, 1))
+    dev = _tensors("kv_pages_copy", (src, torch.int32, 1), (dst, torch.int32, 1))
     if src.numel() != dst.numel():
         _refuse("kv_pages_copy", f"{src.numel()} sources and {dst.numel()} targets")
-    _check(lib().i4_kv_pages_copy(arr, len(pools), num_pages, Hkv, P, D, _p(src), _p(dst), src.numel(), _stream(stream)),
-           "kv_pages_copy")
+    _check(lib().i4_kv_pages_copy(arr, len(pools), num_pages, Hkv, P, D, src.data_ptr(), dst.data_ptr(), src.numel(),
+                                  _raw_stream(stream, dev)), "kv_pages_copy")
 
 
 def kv_pages_reserve(page_table, ctx_len, refs, page_size: int, seqs, add, status=None, ws=None, stream=None):
@@ -481,10 +503,10 @@ def kv_pages_reserve(page_table, ctx_len, refs, page_size: int, seqs, add, statu
     import torch
     if status is None:
         status = torch.empty_like(seqs)
-    desc = _cache_desc("kv_pages_reserve", page_table, ctx_len, refs, page_size, seqs, add, status)
     ws = _kv_ws(ws, page_table, refs)
-    _check(lib().i4_kv_pages_reserve(ctypes.byref(desc), _p(seqs), _p(add), seqs.numel(), _p(status), _p(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_reserve")
+    desc, dev = _cache_desc("kv_pages_reserve", page_table, ctx_len, refs, page_size, ws, seqs, add, status)
+    _check(lib().i4_kv_pages_reserve(ctypes.byref(desc), seqs.data_ptr(), add.data_ptr(), seqs.numel(), status.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "kv_pages_reserve")
     return status
 
 
@@ -495,19 +517,20 @@ def kv_pages_fork(pools, page_table, ctx_len, refs, src, dst, status=None, ws=No
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_fork", pools)
     if status is None:
         status = torch.empty_like(src)
-    desc = _cache_desc("kv_pages_fork", page_table, ctx_len, refs, P, src, dst, status)
+    ws = _kv_ws(ws, page_table, refs)
+    desc, dev = _cache_desc("kv_pages_fork", page_table, ctx_len, refs, P, ws, src, dst, status)
     if refs.numel() != num_pages:
         _refuse("kv_pages_fork", f"{refs.numel()} reference counts for {num_pages} pages")
-    ws = _kv_ws(ws, page_table, refs)
-    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr, len(pools), Hkv, D, _p(src), _p(dst), src.numel(), _p(status),
-                                  _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_fork")
+    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr, len(pools), Hkv, D, src.data_ptr(), dst.data_ptr(), src.numel(),
+                                  status.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "kv_pages_fork")
     return status
 
 
 def kv_pages_free(page_table, ctx_len, refs, page_size: int, seqs, stream=None):
     """The pages of the sequences are given back; their rows become -1 and their ctx_len 0."""
-    desc = _cache_desc("kv_pages_free", page_table, ctx_len, refs, page_size, seqs)
-    _check(lib().i4_kv_pages_free(ctypes.byref(desc), _p(seqs), seqs.numel(), _stream(stream)), "kv_pages_free")
+    desc, dev = _cache_desc("kv_pages_free", page_table, ctx_len, refs, page_size, None, seqs)
+    _check(lib().i4_kv_pages_free(ctypes.byref(desc), seqs.data_ptr(), seqs.numel(), _raw_stream(stream, dev)),
+           "kv_pages_free")
 
 
 def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, stream=None):
@@ -517,12 +540,12 @@ def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, str
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_compact", pools)
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    desc = _cache_desc("kv_pages_compact", page_table, ctx_len, refs, P, n_live)
+    ws = _kv_ws(ws, page_table, refs)
+    desc, dev = _cache_desc("kv_pages_compact", page_table, ctx_len, refs, P, ws, n_live)
     if refs.numel() != num_pages or n_live.numel() != 1:
         _refuse("kv_pages_compact", f"{refs.numel()} reference counts for {num_pages} pages, n_live of {n_live.numel()}")
-    ws = _kv_ws(ws, page_table, refs)
-    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr, len(pools), Hkv, D, _p(n_live), _p(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)), "kv_pages_compact")
+    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr, len(pools), Hkv, D, n_live.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), _raw_stream(stream, dev)), "kv_pages_compact")
     return n_live
 
 

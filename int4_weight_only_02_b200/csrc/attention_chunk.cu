@@ -72,7 +72,8 @@ struct ChunkAttnParams {
     uint16_t *out;
     int T, B, Hq, Hkv, page_size, max_pages, num_pages, window;
     float scale;
-    int slot_tokens;  // 128 / G
+    int slot_tokens;      // 128 / G
+    unsigned unit_inv;    // ceil(2^32 / (NQ * slot_tokens))
     Cut *cuts;        // [kMaxCtas]
     float2 *part_ml;  // [2 * CTAs][unit rows]: (m in powers of two, l)
     float *part_o;    // [2 * CTAs][unit rows][128]
@@ -88,6 +89,17 @@ __device__ __forceinline__ int2 seen(const ChunkAttnParams &p, int pos0, int a, 
 }
 __device__ __forceinline__ int2 tiles_of(int2 s) {
     return s.y > s.x ? make_int2(s.x / kTile, (s.y + kTile - 1) / kTile) : make_int2(0, 0);
+}
+
+// Units of n tokens: ceil(n / unit). n < 2^21 and a unit has at most 256 tokens, so the product is exact.
+template <int NQ>
+__device__ __forceinline__ int units_of(const ChunkAttnParams &p, int n) {
+    return (int)__umulhi((unsigned)(n + NQ * p.slot_tokens - 1), p.unit_inv);
+}
+
+// a * b / c; in 32 bits, which takes a tenth of the time, wherever the line is shorter than 2^23 tiles (b <= 2^9).
+__device__ __forceinline__ long long share(long long a, int b, long long c) {
+    return a < (1 << 23) ? (long long)((unsigned)a * (unsigned)b / (unsigned)c) : a * b / c;
 }
 
 // A CTA's stretch of the line.
@@ -115,14 +127,14 @@ struct Walker {
     __device__ Walker(const ChunkAttnParams &p_, const Stretch &s)
         : p(p_), unit(NQ * p_.slot_tokens), g(s.g), b(s.b), i(s.i), off(s.off), left(s.left), n(s.n), pos0(s.pos0),
           row0(s.row0) {
-        units = (n + unit - 1) / unit;
+        units = units_of<NQ>(p, n);
     }
     __device__ void load() {
         const int2 r = chunk_rows(p.q_start, b, p.T);
         row0 = r.x;
         n = r.y;
         pos0 = max(p.ctx_len[b], 0) - n;
-        units = (n + unit - 1) / unit;
+        units = units_of<NQ>(p, n);
     }
     __device__ bool next(Piece &pc) {
         constexpr int V = Cfg<NQ>::kUnitCost;  // a unit's cost lies on the line as V, then its tiles
@@ -203,19 +215,23 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
         p.cuts[blockIdx.x].valid = 0;
     }
     long long W = 0, start = 0, end = 0;
-    int n_ctas = 1, line = 0;
+    int n_ctas = 1, line = 0, head = 0, target = 0, head_end = 0, target_end = 0;  // kv heads and places of the borders
     int cost = 0, at = 0, j = 0, i = 0;  // this thread's unit: unit i of sequence b0 + j
+    // The CTA whose stretch has the tile before x: the largest c with c W / n <= x - 1.
+    auto last_cta = [&](long long x) {
+        return W < (1 << 23) ? (int)(((unsigned)x * (unsigned)n_ctas - 1u) / (unsigned)W) : (int)((x * n_ctas - 1) / W);
+    };
     // The unit that a border of the stretch lies in, for the thread that has it: a short unit goes whole to the CTA behind.
-    auto offset = [&](long long border) {
-        const int off = (int)(border % line) - at;
+    auto offset = [&](int place_in_line) {
+        const int off = place_in_line - at;
         return off < 0 || off >= cost ? -1 : (cost <= V + C::kWhole ? 0 : off);
     };
     auto place = [&](int b0) {
-        const int off = offset(start);
+        const int off = offset(target);
         if (off >= 0) {
             const int2 seq = chunk_rows(p.q_start, b0 + j, p.T);
-            const long long unit = start - (start % line - at);  // where the unit begins
-            out->g = (int)(start / line);
+            const long long unit = start - (target - at);  // where the unit begins
+            out->g = head;
             out->b = b0 + j;
             out->i = i;
             out->off = off;
@@ -223,13 +239,12 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
             out->pos0 = pos[j];
             out->row0 = seq.x;
             atomicSub(&out->left, (int)(unit + off - start));
-            if (off > V && W * (blockIdx.x - 1) / n_ctas <= unit + V)
+            if (off > V && share(W, blockIdx.x - 1, n_ctas) <= unit + V)
                 // the first cut of this unit: its parts end in the CTA that holds its last tile
-                p.cuts[blockIdx.x] = {1, (int)(((unit + cost) * n_ctas - 1) / W), min(seq.y - i * size, size), seq.x + i * size,
-                                      (int)(start / line)};
+                p.cuts[blockIdx.x] = {1, last_cta(unit + cost), min(seq.y - i * size, size), seq.x + i * size, head};
         }
-        const int off_end = end < W ? offset(end) : -1;
-        if (off_end >= 0) atomicAdd(&out->left, off_end - (int)(end % line - at));
+        const int off_end = end < W ? offset(target_end) : -1;
+        if (off_end >= 0) atomicAdd(&out->left, off_end - (target_end - at));
     };
     for (int pass = 0; pass < 2; ++pass) {  // the first measures the line, the second finds the place in it
         int run = 0, trips = 0;
@@ -239,7 +254,7 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
                 n = chunk_rows(p.q_start, b0 + tid, p.T).y;
                 first_pos = max(p.ctx_len[b0 + tid], 0) - n;
             }
-            const int before = scan_block<NT>((n + size - 1) / size, total_units, sums);
+            const int before = scan_block<NT>(units_of<NQ>(p, n), total_units, sums);
             first[tid] = before;
             tokens[tid] = n;
             pos[tid] = first_pos;
@@ -273,9 +288,13 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
             line = run;
             W = (long long)line * p.Hkv;
             n_ctas = (int)min((long long)gridDim.x, max((W + C::kMinCost - 1) / C::kMinCost, 1ll));
-            start = W * blockIdx.x / n_ctas;
-            end = W * (blockIdx.x + 1) / n_ctas;
+            start = share(W, blockIdx.x, n_ctas);
+            end = share(W, blockIdx.x + 1, n_ctas);
             if ((int)blockIdx.x >= n_ctas || start >= end) break;
+            head = (int)share(start, 1, line);
+            target = (int)(start - (long long)head * line);
+            head_end = (int)share(end, 1, line);
+            target_end = (int)(end - (long long)head_end * line);
             if (tid == 0) out->left = (int)(end - start);
             __syncthreads();
             if (trips == 1 && p.B <= NT) {  // every unit is still in its thread's hands
@@ -614,8 +633,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 to[k] = __shfl_sync(0xffffffffu, mine ? ((long long)(last.row0 + tok) * p.Hq + head) * 128 : -1ll, (lane & ~3) + k);
-            float bad = 0.f;  // stays 0 while every value of O is finite
-#pragma unroll 1
+            float bad[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while every value of O is finite
+#pragma unroll 2
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
                 if (any) {
@@ -626,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) bad = fmaf(__uint_as_float(o[i]), 0.f, bad);
+                for (int i = 0; i < 32; ++i) bad[i & 3] = fmaf(__uint_as_float(o[i]), 0.f, bad[i & 3]);
                 if (last.whole) {
                     uint4 v[4];  // 16-byte chunks 4c .. 4c + 3 of this lane's row
 #pragma unroll
@@ -662,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 if (lane == 0) mbar_arrive(&o_free[s]);
             }
             // rows that met a NaN or an infinity, and whose own scores are fine, are summed again over what they see
-            unsigned again = __ballot_sync(0xffffffffu, mine && any && !(bad == 0.f) && fabsf(l) < INFINITY);
+            unsigned again = __ballot_sync(0xffffffffu, mine && any && !(bad[0] + bad[1] + (bad[2] + bad[3]) == 0.f) && fabsf(l) < INFINITY);
             while (again) {
                 const int k = __ffs(again) - 1;
                 again &= again - 1;
@@ -908,7 +927,9 @@ static int device_sms(int *sms) {
 }
 
 template <int NQ>
-static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkAttnParams &p, int sms, cudaStream_t stream) {
+static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, ChunkAttnParams p, int sms, cudaStream_t stream) {
+    const unsigned unit = NQ * p.slot_tokens;
+    p.unit_inv = (unsigned)((0x100000000ull + unit - 1) / unit);
     const int grid = sms * Cfg<NQ>::kCtasPerSm;
     chunk_attn_kernel<NQ><<<grid, Cfg<NQ>::kThreads, Cfg<NQ>::kSmem, stream>>>(tq, tk, tv, p);
     int st = launch_check("i4_paged_gqa_chunk");
