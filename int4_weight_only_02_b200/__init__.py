@@ -13,6 +13,7 @@ per word, field i at bits 4i..4i+3, two's complement), fp16 group-128 scales
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -65,7 +66,7 @@ class KvCacheDesc(ctypes.Structure):
                 ("page_size", _i), ("num_pages", _i)]
 
 
-_ll, _d, _pools = ctypes.c_longlong, ctypes.c_double, ctypes.POINTER(_vp)
+_ll, _d = ctypes.c_longlong, ctypes.c_double
 
 _SIGS = {
     "i4_last_error": (ctypes.c_char_p, []),
@@ -94,11 +95,11 @@ _SIGS = {
     "i4_paged_gqa_chunk": (_i, [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz,
                                 _vp]),
     "i4_kv_pages_ws_bytes": (_sz, [_i, _i]),
-    "i4_kv_pages_copy": (_i, [_pools, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]),
+    "i4_kv_pages_copy": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]),
     "i4_kv_pages_reserve": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _vp, _i, _vp, _vp, _sz, _vp]),
-    "i4_kv_pages_fork": (_i, [ctypes.POINTER(KvCacheDesc), _pools, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_fork": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
     "i4_kv_pages_free": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _vp]),
-    "i4_kv_pages_compact": (_i, [ctypes.POINTER(KvCacheDesc), _pools, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_compact": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "decode_step_graph_create": (_i, [ctypes.POINTER(ModelDesc), ctypes.POINTER(ModelWeights),
                                       ctypes.POINTER(SeqState), ctypes.POINTER(_vp)]),
     "decode_step_graph_replay": (_i, [_vp, _vp]),
@@ -440,7 +441,7 @@ def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, w
 
 
 def _pool_array(name: str, pools):
-    """(host array of the pools' addresses, shape of a pool) of a sequence of equal pools of 16-bit values."""
+    """(host array of the pools' addresses, shape of the first) of a sequence of equal pools of 16-bit values."""
     import torch
     T = torch.Tensor
     shape = pools[0].shape if len(pools) else ()
@@ -449,10 +450,10 @@ def _pool_array(name: str, pools):
     dev = pools[0].get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         _refuse(name, f"pools on the current CUDA device are needed, got {pools[0].device}")
-    if (set(map(T.size, pools)) != {shape} or set(map(T.element_size, pools)) != {2} or not all(map(T.is_contiguous, pools))
-            or set(map(T.get_device, pools)) != {dev}):
-        _refuse(name, "pools of one shape, two bytes a value, contiguous and on one device are needed")
-    return (_vp * len(pools))(*map(T.data_ptr, pools)), shape
+    if (set(map(T.numel, pools)) != {pools[0].numel()} or set(map(T.element_size, pools)) != {2}
+            or not all(map(T.is_contiguous, pools)) or set(map(T.get_device, pools)) != {dev}):
+        _refuse(name, "pools of one size, two bytes a value, contiguous and on one device are needed")
+    return array.array("Q", map(T.data_ptr, pools)), shape
 
 
 def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, ws, *lists):
@@ -493,7 +494,7 @@ def kv_pages_copy(pools, src, dst, stream=None):
     dev = _tensors("kv_pages_copy", (src, torch.int32, 1), (dst, torch.int32, 1))
     if src.numel() != dst.numel():
         _refuse("kv_pages_copy", f"{src.numel()} sources and {dst.numel()} targets")
-    _check(lib().i4_kv_pages_copy(arr, len(pools), num_pages, Hkv, P, D, src.data_ptr(), dst.data_ptr(), src.numel(),
+    _check(lib().i4_kv_pages_copy(arr.buffer_info()[0], len(pools), num_pages, Hkv, P, D, src.data_ptr(), dst.data_ptr(), src.numel(),
                                   _raw_stream(stream, dev)), "kv_pages_copy")
 
 
@@ -521,7 +522,7 @@ def kv_pages_fork(pools, page_table, ctx_len, refs, src, dst, status=None, ws=No
     desc, dev = _cache_desc("kv_pages_fork", page_table, ctx_len, refs, P, ws, src, dst, status)
     if refs.numel() != num_pages:
         _refuse("kv_pages_fork", f"{refs.numel()} reference counts for {num_pages} pages")
-    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr, len(pools), Hkv, D, src.data_ptr(), dst.data_ptr(), src.numel(),
+    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr.buffer_info()[0], len(pools), Hkv, D, src.data_ptr(), dst.data_ptr(), src.numel(),
                                   status.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "kv_pages_fork")
     return status
 
@@ -544,7 +545,7 @@ def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, str
     desc, dev = _cache_desc("kv_pages_compact", page_table, ctx_len, refs, P, ws, n_live)
     if refs.numel() != num_pages or n_live.numel() != 1:
         _refuse("kv_pages_compact", f"{refs.numel()} reference counts for {num_pages} pages, n_live of {n_live.numel()}")
-    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr, len(pools), Hkv, D, n_live.data_ptr(), ws.data_ptr(),
+    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr.buffer_info()[0], len(pools), Hkv, D, n_live.data_ptr(), ws.data_ptr(),
                                      ws.numel(), _raw_stream(stream, dev)), "kv_pages_compact")
     return n_live
 

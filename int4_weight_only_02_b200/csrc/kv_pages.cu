@@ -19,6 +19,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxSeqs = 16384;      // a 64 KB table of owners in shared memory
 constexpr int kMaxPages = 1 << 20;   // a sum over 1024 requests of at most this many pages fits 31 bits
 constexpr int kPoolsPerLaunch = 256;  // pool addresses in the kernel's parameters
+constexpr int kLanePages = 8;         // page ids that a lane has in flight: a row of 256 pages costs one latency, not eight
 
 struct PoolPtrs {
     unsigned char *p[kPoolsPerLaunch];
@@ -67,7 +68,7 @@ __device__ __forceinline__ int find_free(const int32_t *refs, int num_pages, int
         const int p = p0 + 4 * threadIdx.x;
         int r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = p + i < num_pages ? __ldcg(refs + p + i) : 1;  // written by atomics: past L1
+        for (int i = 0; i < 4; ++i) r[i] = p + i < num_pages ? *(volatile const int32_t *)(refs + p + i) : 1;  // written by atomics
         int total;
         int at = found + block_scan((r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0), total, sm);
 #pragma unroll
@@ -156,12 +157,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const CacheArg
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c, const int32_t *src, const int32_t *dst, int n,
-                                                               int32_t *status, Lists ws) {
-    extern __shared__ int owner[];
+                                                               int32_t *status, Lists ws, int smem_refs) {
+    grid_dep_launch();  // the copy may come up; it waits for this kernel's end before it reads anything
+    extern __shared__ int owner[];  // [S], then the counts of the pages where they fit
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t kNone = n;
+    int32_t *refs = smem_refs ? owner + c.S : c.refs;
     for (int s = tid; s < c.S; s += kPlanThreads) owner[s] = kNone;
+    if (smem_refs)
+        for (int p = tid; p < c.num_pages; p += kPlanThreads) refs[p] = c.refs[p];
     __syncthreads();
     for (int i = tid; i < n; i += kPlanThreads)
         if (dst[i] >= 0 && dst[i] < c.S) atomicMin(&owner[dst[i]], i);
@@ -176,10 +181,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
         const int32_t *old = c.table + (size_t)dst[i] * c.max_pages, *row = c.table + (size_t)src[i] * c.max_pages;
         const int held = pages_of(c.ctx_len[dst[i]], c.P, c.max_pages);
         const int full = min(max(c.ctx_len[src[i]], 0) / c.P, c.max_pages);
-        for (int j = lane; j < max(held, full); j += 32) {
-            const int a = j < held ? old[j] : -1, b = j < full ? row[j] : -1;
-            if (a >= 0 && a < c.num_pages) atomicSub(&c.refs[a], 1);
-            if (b >= 0 && b < c.num_pages) atomicAdd(&c.refs[b], 1);
+        for (int j0 = lane; j0 < max(held, full); j0 += 32 * kLanePages) {
+            int a[kLanePages], b[kLanePages];
+#pragma unroll
+            for (int k = 0; k < kLanePages; ++k) {
+                const int j = j0 + 32 * k;
+                a[k] = j < held ? old[j] : -1;
+                b[k] = j < full ? row[j] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kLanePages; ++k) {
+                if (a[k] >= 0 && a[k] < c.num_pages) atomicSub(&refs[a[k]], 1);
+                if (b[k] >= 0 && b[k] < c.num_pages) atomicAdd(&refs[b[k]], 1);
+            }
         }
     }
     __syncthreads();
@@ -197,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
         if (i < n) ws.b[i] = need ? at : -1;
         want += total;
     }
-    const int have = find_free(c.refs, c.num_pages, want, ws.a, sm);
+    const int have = find_free(refs, c.num_pages, want, ws.a, sm);
     for (int i = warp; i < n; i += kPlanThreads / 32) {
         const bool ok = valid(i);
         const int at = ws.b[i];
@@ -209,10 +223,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
             int32_t *out = c.table + (size_t)dst[i] * c.max_pages;
             const int ctx = min(max(c.ctx_len[src[i]], 0), c.max_pages * c.P), full = ctx / c.P;
             if (room) {
-                for (int j = lane; j < c.max_pages; j += 32) out[j] = j < full ? row[j] : -1;
+                for (int j0 = lane; j0 < c.max_pages; j0 += 32 * kLanePages) {
+                    int a[kLanePages];
+#pragma unroll
+                    for (int k = 0; k < kLanePages; ++k) a[k] = j0 + 32 * k < full ? row[j0 + 32 * k] : -1;
+#pragma unroll
+                    for (int k = 0; k < kLanePages; ++k)
+                        if (j0 + 32 * k < c.max_pages) out[j0 + 32 * k] = a[k];
+                }
             } else {  // no page left: the target stays empty and holds nothing
                 for (int j = lane; j < full; j += 32)
-                    if (row[j] >= 0 && row[j] < c.num_pages) atomicSub(&c.refs[row[j]], 1);
+                    if (row[j] >= 0 && row[j] < c.num_pages) atomicSub(&refs[row[j]], 1);
                 for (int j = lane; j < c.max_pages; j += 32) out[j] = -1;
             }
             if (at >= 0 && room) {
@@ -224,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
             if (lane == 0) {
                 if (at >= 0 && room) {
                     out[full] = to;
-                    c.refs[to] = 1;
+                    refs[to] = 1;
                 }
                 c.ctx_len[dst[i]] = room ? ctx : 0;
             }
@@ -235,6 +256,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
             ws.c[n + i] = fill;
             if (status) status[i] = !ok ? 2 : (room ? 0 : 1);
         }
+    }
+    if (smem_refs) {
+        __syncthreads();
+        for (int p = tid; p < c.num_pages; p += kPlanThreads) c.refs[p] = refs[p];
     }
 }
 
@@ -260,6 +285,7 @@ __global__ void kv_free_kernel(const CacheArgs c, const int32_t *seqs, int n) {
 // a: target, b: source of each move; c[p]: the new id of a page p >= n_live.
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(int32_t *refs, int num_pages, int32_t *n_live_out,
                                                                       Lists ws) {
+    grid_dep_launch();
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x;
     int mine = 0, n_live;
@@ -318,13 +344,25 @@ __device__ __forceinline__ void copy_span(unsigned char *dst, const unsigned cha
         if (v0 + u * kCopyThreads < vecs) __stcs(reinterpret_cast<uint4 *>(dst) + v0 + u * kCopyThreads, v[u]);
 }
 
-// Whole pages src[i] -> dst[i] of every pool; n_dev, when given, is the device's count. Work item: (pool, i, part).
+// Whole pages src[i] -> dst[i] of every pool; n_dev, when given, is the device's count. Work item: (pool, i, part). The first
+// remap_blocks blocks instead give table entries of held pages at or above n_live (n_dev[1]) the page's new id.
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ PoolPtrs pools, int n_pools, const int32_t *src,
                                                                const int32_t *dst, int n, const int32_t *n_dev, int num_pages,
-                                                               int page_vecs, int parts) {
+                                                               int page_vecs, int parts, const CacheArgs c, const int32_t *new_id,
+                                                               int remap_blocks) {
+    grid_dep_wait();
+    if ((int)blockIdx.x < remap_blocks) {
+        const int n_live = n_dev[1];
+        const long long entries = (long long)c.S * c.max_pages;
+        for (long long x = blockIdx.x * (long long)kCopyThreads + threadIdx.x; x < entries; x += (long long)remap_blocks * kCopyThreads) {
+            const int s = (int)(x / c.max_pages), j = (int)(x % c.max_pages), p = c.table[x];
+            if (j < pages_of(c.ctx_len[s], c.P, c.max_pages) && p >= n_live && p < c.num_pages) c.table[x] = new_id[p];
+        }
+        return;
+    }
     if (n_dev) n = min(n, *n_dev);
     const long long items = (long long)n_pools * n * parts;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    for (long long it = blockIdx.x - remap_blocks; it < items; it += gridDim.x - remap_blocks) {
         const int part = (int)(it % parts);
         const long long r = it / parts;
         const int i = (int)(r % n), pool = (int)(r / n);
@@ -339,6 +377,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid_constant__ PoolPtrs pools, int n_pools,
                                                                     const int32_t *from, const int32_t *to, const int32_t *fill, int n,
                                                                     int Hkv, int P, int row_vecs, int parts) {
+    grid_dep_wait();
     const long long items = (long long)n_pools * n * parts;
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
         const int part = (int)(it % parts);
@@ -362,18 +401,6 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u)
             if ((part * kCopyUnroll + u) * kCopyThreads + (int)threadIdx.x < vecs) __stcs(d + at[u], v[u]);
-    }
-}
-
-// Table entries of held pages at or above n_live take the page's new id.
-__global__ void kv_remap_kernel(const CacheArgs c, Lists ws) {
-    const int n_live = ws.count[1];
-    const long long n = (long long)c.S * c.max_pages;
-    for (long long x = blockIdx.x * (long long)blockDim.x + threadIdx.x; x < n; x += (long long)gridDim.x * blockDim.x) {
-        const int s = (int)(x / c.max_pages), j = (int)(x % c.max_pages);
-        if (j >= pages_of(c.ctx_len[s], c.P, c.max_pages)) continue;
-        const int p = c.table[x];
-        if (p >= n_live && p < c.num_pages) c.table[x] = ws.c[p];
     }
 }
 
@@ -424,30 +451,38 @@ static CacheArgs cache_args(const i4_kv_cache *c) {
     return {c->page_table, c->ctx_len, c->refs, c->n_seqs, c->max_pages_per_seq, c->page_size, c->num_pages};
 }
 
-// The plan kernels keep one int per sequence in dynamic shared memory, above 48 KB from 12289 sequences on; the attribute
-// belongs to the current device, and setting it again costs little beside a launch.
+// The plan kernels keep an int per sequence, and the fork one per page too where they fit, in dynamic shared memory: many
+// targets of one source count the same pages up and down, and 63 of them over 251 pages took 17 us on global atomics. The
+// attribute that allows more than 48 KB belongs to the current device, and setting it again costs little beside a launch.
+constexpr size_t kPlanSmem = 200 * 1024;
 template <typename K>
-static int owner_smem(K kernel, int n_seqs, size_t *bytes, const char *what) {
-    *bytes = (size_t)n_seqs * sizeof(int);
-    if (*bytes <= 47 * 1024) return I4_OK;
-    return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes), what);
+static int plan_smem(K kernel, size_t bytes, const char *what) {
+    if (bytes <= 47 * 1024) return I4_OK;
+    return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what);
 }
 
 static int copy_grid(long long items) {
-    const long long most = 16ll * kNumSMs;
+    const long long most = 32ll * kNumSMs;
     return (int)(items < most ? (items > 0 ? items : 1) : most);
 }
 
 static int launch_copy(void *const *pools, int n_pools, const int32_t *src, const int32_t *dst, int n, const int32_t *n_dev,
-                       int num_pages, long long page_bytes, cudaStream_t stream, const char *what) {
+                       int num_pages, long long page_bytes, const CacheArgs *remap, const int32_t *new_id, cudaStream_t stream,
+                       const char *what) {
     const int vecs = (int)(page_bytes / 16), parts = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
     for (int p0 = 0; p0 < n_pools; p0 += kPoolsPerLaunch) {
         PoolPtrs pp;
         const int m = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
-        kv_copy_kernel<<<copy_grid((long long)m * n * parts), kCopyThreads, 0, stream>>>(pp, m, src, dst, n, n_dev, num_pages, vecs,
-                                                                                       parts);
-        const int st = launch_check(what);
+        int blocks = 0;
+        if (remap && p0 == 0) {
+            const long long b = ((long long)remap->S * remap->max_pages + kCopyThreads - 1) / kCopyThreads;
+            blocks = (int)(b < kNumSMs ? b : kNumSMs);
+        }
+        const int st = cuda_check(launch(kv_copy_kernel, dim3(blocks + copy_grid((long long)m * n * parts)), dim3(kCopyThreads), 0, stream,
+                                         n_dev != nullptr && p0 == 0, pp, m, src, dst, n, n_dev, num_pages, vecs, parts,
+                                         remap ? *remap : CacheArgs{}, new_id, blocks),
+                                  what);
         if (st) return st;
     }
     return I4_OK;
@@ -470,8 +505,8 @@ extern "C" int i4_kv_pages_copy(void *const *pools, int n_pools, int num_pages, 
     if (n == 0) return I4_OK;
     if (!src || !dst) return fail(I4_EINVAL, "i4_kv_pages_copy: null pointer");
     if (!aligned(src, 4) || !aligned(dst, 4)) return fail(I4_EALIGN, "i4_kv_pages_copy: lists must be 4-byte aligned");
-    return launch_copy(pools, n_pools, src, dst, n, nullptr, num_pages, (long long)Hkv * page_size * D * 2, (cudaStream_t)stream,
-                       "i4_kv_pages_copy");
+    return launch_copy(pools, n_pools, src, dst, n, nullptr, num_pages, (long long)Hkv * page_size * D * 2, nullptr,
+                       nullptr, (cudaStream_t)stream, "i4_kv_pages_copy");
 }
 
 extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs, const int32_t *add, int n, int32_t *status, void *ws,
@@ -481,8 +516,8 @@ extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs
     if (!st) st = check_ws("i4_kv_pages_reserve", ws, ws_bytes, cache->num_pages, cache->n_seqs);
     if (st || n == 0) return st;
     if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_reserve: %d requests for %d sequences", n, cache->n_seqs);
-    size_t smem;
-    if ((st = owner_smem(kv_reserve_kernel, cache->n_seqs, &smem, "i4_kv_pages_reserve"))) return st;
+    const size_t smem = (size_t)cache->n_seqs * sizeof(int);
+    if ((st = plan_smem(kv_reserve_kernel, smem, "i4_kv_pages_reserve"))) return st;
     kv_reserve_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), seqs, add, n, status,
                                                                        ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs)));
     return launch_check("i4_kv_pages_reserve");
@@ -496,10 +531,12 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
     if (!st) st = check_ws("i4_kv_pages_fork", ws, ws_bytes, cache->num_pages, cache->n_seqs);
     if (st || n == 0) return st;
     if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_fork: %d forks for %d sequences", n, cache->n_seqs);
-    size_t smem;
-    if ((st = owner_smem(kv_fork_kernel, cache->n_seqs, &smem, "i4_kv_pages_fork"))) return st;
+    size_t smem = ((size_t)cache->n_seqs + cache->num_pages) * sizeof(int);
+    const int smem_refs = smem <= kPlanSmem;
+    if (!smem_refs) smem = (size_t)cache->n_seqs * sizeof(int);
+    if ((st = plan_smem(kv_fork_kernel, smem, "i4_kv_pages_fork"))) return st;
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
-    kv_fork_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), src, dst, n, status, L);
+    kv_fork_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), src, dst, n, status, L, smem_refs);
     if ((st = launch_check("i4_kv_pages_fork"))) return st;
     const int row_vecs = D / 8, vecs = Hkv * cache->page_size * row_vecs;
     const int parts = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
@@ -507,9 +544,11 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
         PoolPtrs pp;
         const int m = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
-        kv_copy_rows_kernel<<<copy_grid((long long)m * n * parts), kCopyThreads, 0, (cudaStream_t)stream>>>(
-            pp, m, L.b, L.c, L.c + n, n, Hkv, cache->page_size, row_vecs, parts);
-        if ((st = launch_check("i4_kv_pages_fork copy"))) return st;
+        st = cuda_check(launch(kv_copy_rows_kernel, dim3(copy_grid((long long)m * n * parts)), dim3(kCopyThreads), 0, (cudaStream_t)stream,
+                               p0 == 0, pp, m, (const int32_t *)L.b, (const int32_t *)L.c, (const int32_t *)L.c + n, n, Hkv,
+                               cache->page_size, row_vecs, parts),
+                        "i4_kv_pages_fork copy");
+        if (st) return st;
     }
     return I4_OK;
 }
@@ -531,9 +570,7 @@ extern "C" int i4_kv_pages_compact(const i4_kv_cache *cache, void *const *pools,
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
     kv_compact_plan_kernel<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(cache->refs, cache->num_pages, n_live, L);
     if ((st = launch_check("i4_kv_pages_compact plan"))) return st;
-    const long long entries = (long long)cache->n_seqs * cache->max_pages_per_seq;
-    kv_remap_kernel<<<copy_grid((entries + 255) / 256), 256, 0, (cudaStream_t)stream>>>(cache_args(cache), L);
-    if ((st = launch_check("i4_kv_pages_compact tables"))) return st;
+    const CacheArgs args = cache_args(cache);
     return launch_copy(pools, n_pools, L.b, L.a, cache->num_pages, L.count, cache->num_pages,
-                       (long long)Hkv * cache->page_size * D * 2, (cudaStream_t)stream, "i4_kv_pages_compact");
+                       (long long)Hkv * cache->page_size * D * 2, &args, L.c, (cudaStream_t)stream, "i4_kv_pages_compact");
 }

@@ -44,10 +44,23 @@ struct RopeChunkParams {
 
 // One CTA per token. Sixteen lanes take one head, eight values (16 bytes) each, and a lane's partner values come
 // from the lane rd/16 away by shuffles (half layout) or are its own neighbours (interleaved). The angles of a lane are
-// the same for every head, so they are read once.
+// the same for every head, so they are read once. Bound by HBM for many tokens and by the chain of dependent loads
+// (sequence, position, page and angles) for few: the first two heads' values, which depend on none of it, are loaded first.
 template <bool kInterleaved>
 __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkParams p) {
     const int t = blockIdx.x;
+    const int c = threadIdx.x & 15;  // 16-byte chunk of the head
+    const int heads = p.Hq + 2 * p.Hkv, step = blockDim.x >> 4, h_first = threadIdx.x >> 4;
+    const uint16_t *src = p.qkv + (size_t)t * p.qkv_stride + 8 * c;
+    uint4 v[2];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (h0 + k * step < heads) v[k] = __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(h0 + k * step) * 128));
+        }
+    };
+    load(h_first);
     const int b = chunk_find(p.q_start, p.B, t);
     if (b >= p.B) return;  // a row behind the last sequence
     const int2 rows = chunk_rows(p.q_start, b, p.T);
@@ -56,7 +69,6 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
     const int page = p.page_table[(size_t)b * p.max_pages + pos / p.page_size], slot = pos % p.page_size;
     const bool page_ok = page >= 0 && page < p.num_pages;
 
-    const int c = threadIdx.x & 15;      // 16-byte chunk of the head
     const int h16 = p.rd / 16;           // chunks of one half of the rotated part
     const bool turn = c < 2 * h16;
     const bool low = c < h16;
@@ -66,19 +78,18 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
     const float2 *row = p.cs + (size_t)pos * (p.rd / 2);
 #pragma unroll
     for (int i = 0; i < (kInterleaved ? 4 : 8); i += 2) {
-        float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+        float4 a = make_float4(1.f, 0.f, 1.f, 0.f);
         if (turn)
-            v = *reinterpret_cast<const float4 *>(row + (kInterleaved ? 4 * c : 8 * (low ? c : c - h16)) + i);
-        cs[i] = make_float2(v.x, v.y);
-        cs[i + 1] = make_float2(v.z, v.w);
+            a = *reinterpret_cast<const float4 *>(row + (kInterleaved ? 4 * c : 8 * (low ? c : c - h16)) + i);
+        cs[i] = make_float2(a.x, a.y);
+        cs[i + 1] = make_float2(a.z, a.w);
     }
-    const int heads = p.Hq + 2 * p.Hkv, step = blockDim.x >> 4;
-    const uint16_t *src = p.qkv + (size_t)t * p.qkv_stride + 8 * c;
-    for (int h0 = 0; h0 < heads; h0 += step) {  // the same trips for every thread: the shuffles need whole warps
-        const int h = h0 + (threadIdx.x >> 4);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (h < heads) v = *reinterpret_cast<const uint4 *>(src + (size_t)h * 128);
-        uint32_t x[4] = {v.x, v.y, v.z, v.w}, y[4];
+    for (int h0 = h_first; h0 - h_first < heads; h0 += 2 * step) {  // the same trips for every thread: the shuffles need whole warps
+        if (h0 != h_first) load(h0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+        const int h = h0 + k * step;
+        uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, y[4];
         if (kInterleaved) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -110,6 +121,7 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
             dst = (h < p.Hq + p.Hkv ? p.k_pool : p.v_pool) + (((size_t)page * p.Hkv + g) * p.page_size + slot) * 128;
         }
         *reinterpret_cast<uint4 *>(dst + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
     }
 }
 

@@ -214,6 +214,18 @@ def test_many_sequences(i4lib, cuda, n_seqs):
     c.compact()
 
 
+@pytest.mark.parametrize("num_pages", [12000, 52000])
+def test_fork_in_a_large_pool(i4lib, cuda, num_pages):
+    """More page counts than fit beside the sequences in 48 KB, and in the plan's shared memory at all."""
+    c = Both(i4lib, cuda, 30, 20, 8, num_pages, n_pools=1, d=8)
+    c.model.refs[:num_pages - 40] = 1  # held by somebody else: the free pages are the last
+    c.upload()
+    assert c.reserve([0, 1], [150, 33]) == [0, 0]
+    assert c.fork([0, 0, 1, 0], [2, 3, 4, 5]) == [0, 0, 0, 0]
+    assert c.fork([0, 1], [5, 3]) == [0, 0]
+    c.free([0, 3])
+
+
 def test_captured_operations(i4lib, cuda):
     """Reserve, fork and free in one graph, replayed: every replay acts on the cache as it is."""
     import torch
