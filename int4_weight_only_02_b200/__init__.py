@@ -550,4 +550,5 @@ def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, str
     return n_live
 
 
-from .runtime import BatchedDecode, DecodeGraph, DeviceModel, Prefill, Sequence  # noqa: E402,F401
+from .runtime import (BatchedDecode, ChunkedDecoder, DecodeGraph, DeviceModel, PagedCache, Prefill,  # noqa: E402,F401
+                      Sequence)  # noqa: E402,F401

@@ -442,3 +442,161 @@ class Prefill:
             seq.history[n:n + 1].copy_(seq.token, non_blocking=True)
             seq.status.zero_()
         return seq.token
+
+
+def _int_list(v, dev):
+    """A device int32 tensor of a host sequence or tensor."""
+    import torch
+    return torch.as_tensor(v, dtype=torch.int32).to(dev)
+
+
+class PagedCache:
+    """The K/V pages of up to ``n_seqs`` sequences: pools per layer shared by all of them, a page-table row and a length per
+    sequence slot, and how many sequences hold each page. Sequences grow by ``reserve``, continue each other by ``fork``
+    (full pages shared, the last one copied), end by ``free``, and ``compact`` moves the pages in use to the front of the
+    pools. All state is on the device; the calls go to one stream and synchronise nothing."""
+
+    def __init__(self, model: DeviceModel, n_seqs: int, num_pages: int, max_pages_per_seq: int | None = None):
+        import torch
+        from . import kv_pages_ws_bytes
+        s, dev = model.shape, model.device
+        self.model, self.page_size, self.n_seqs, self.num_pages = model, s.page_size, int(n_seqs), int(num_pages)
+        self.max_pages = int(max_pages_per_seq if max_pages_per_seq is not None else s.max_pages)
+        kv = (self.num_pages, s.n_kv, s.page_size, s.head_dim)
+        self.k_pools = [torch.zeros(kv, dtype=torch.float16, device=dev) for _ in range(s.layers)]
+        self.v_pools = [torch.zeros(kv, dtype=torch.float16, device=dev) for _ in range(s.layers)]
+        self.pools = self.k_pools + self.v_pools
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.page_table = torch.full((self.n_seqs, self.max_pages), -1, **i32)
+        self.ctx_len = torch.zeros(self.n_seqs, **i32)
+        self.refs = torch.zeros(self.num_pages, **i32)
+        self.ws = torch.empty(max(kv_pages_ws_bytes(self.num_pages, self.n_seqs), 256), dtype=torch.uint8, device=dev)
+
+    def reserve(self, seqs, add, stream=None):
+        """Room for add[i] more tokens of sequence seqs[i], whose length grows by it; status [n] (see kv_pages_reserve)."""
+        from . import kv_pages_reserve
+        dev = self.refs.device
+        return kv_pages_reserve(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, dev),
+                                _int_list(add, dev), ws=self.ws, stream=stream)
+
+    def fork(self, src, dst, stream=None):
+        """Sequence dst[i] continues src[i]; status [n] (see kv_pages_fork)."""
+        from . import kv_pages_fork
+        dev = self.refs.device
+        return kv_pages_fork(self.pools, self.page_table, self.ctx_len, self.refs, _int_list(src, dev), _int_list(dst, dev),
+                             ws=self.ws, stream=stream)
+
+    def free(self, seqs, stream=None):
+        from . import kv_pages_free
+        kv_pages_free(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, self.refs.device),
+                      stream=stream)
+
+    def compact(self, stream=None):
+        """The number of pages in use, [1] on the device; they are the pools' first ones afterwards."""
+        from . import kv_pages_compact
+        return kv_pages_compact(self.pools, self.page_table, self.ctx_len, self.refs, ws=self.ws, stream=stream)
+
+
+class ChunkedDecoder:
+    """New tokens of several sequences of a PagedCache at once: chunks of prompts of any lengths beside single tokens, up to
+    ``max_tokens`` in a call.
+
+    The new tokens of all sequences are the activation rows of one pass: embedding gather, batched RMSNorm, the INT4
+    linear layers on the tcgen05 GEMM, rotary positions with the append to the pages (``rope_append_chunk``),
+    attention of the chunk over the pages (``paged_gqa_chunk``), SiLU-mul and the residual adds; the final norm and
+    lm_head run for every sequence's last new token. ``scaling``, ``factor`` and ``original_ctx`` extend the context (see
+    ``rope_table``).
+    """
+
+    def __init__(self, model: DeviceModel, cache: PagedCache, max_tokens: int = 512, scaling: str = "none",
+                 factor: float = 1.0, original_ctx: int = 0):
+        import torch
+        from . import paged_gqa_chunk_ws_bytes, rope_table
+        s, dev = model.shape, model.device
+        self.model, self.cache, self.shape = model, cache, s
+        self.n_max = n = int(max_tokens)
+        f16 = dict(dtype=torch.float16, device=dev)
+        self.cs = rope_table(cache.max_pages * s.page_size, s.head_dim, s.theta, scaling, factor, original_ctx, device=dev)
+        self.r = torch.zeros((n, s.hidden), **f16)
+        self.xn = torch.zeros((n, s.hidden), **f16)
+        self.qkv = torch.zeros((n, (s.n_q + 2 * s.n_kv) * s.head_dim), **f16)
+        self.q = torch.zeros((n, s.n_q, s.head_dim), **f16)
+        self.attn = torch.zeros((n, s.n_q, s.head_dim), **f16)
+        self.y = torch.zeros((n, s.hidden), **f16)
+        self.gu = torch.zeros((n, 2 * s.inter), **f16)
+        self.mlp = torch.zeros((n, s.inter), **f16)
+        self.attn_ws = torch.empty(paged_gqa_chunk_ws_bytes(), dtype=torch.uint8, device=dev)
+        self.gemm_ws = _gemm_workspace(s, n, dev)
+        # the split-K layout depends on the row count: room for any up to n
+        from . import int4_gemm_ws_bytes
+        shapes = [(self.qkv.shape[1], s.hidden), (s.hidden, s.n_q * s.head_dim), (2 * s.inter, s.hidden), (s.hidden, s.inter),
+                  (s.vocab, s.hidden)]
+        need = max(int4_gemm_ws_bytes(m, a, b) for m in range(1, n + 1) for a, b in shapes)
+        if need > self.gemm_ws.numel():
+            self.gemm_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+
+    def run(self, chunks: dict, stream=None):
+        """Feeds chunks[seq] (token ids, at least one) to every sequence named; returns (next tokens [len(chunks)] int32,
+        logits [len(chunks)][vocab] fp32) of their last tokens, in ascending order of the sequences. Raises I4Error, with
+        nothing fed, when a sequence's pages do not suffice (which reads the reservation's status from the device)."""
+        import torch
+        from . import (I4_ENOMEM, I4Error, argmax_rows, embed_gather, int4_gemm, paged_gqa_chunk, rmsnorm, rope_append_chunk,
+                       silu_mul)
+        m, s, cache = self.model, self.shape, self.cache
+        g, L, dev = m.glob, m.layers, m.device
+        seqs = sorted(int(k) for k in chunks)
+        toks = [np.asarray(chunks[k], dtype=np.int32).reshape(-1) for k in seqs]
+        lens = np.zeros(cache.n_seqs, dtype=np.int32)
+        if not seqs or seqs[0] < 0 or seqs[-1] >= cache.n_seqs or min(len(t) for t in toks) < 1:
+            raise ValueError(f"sequences 0..{cache.n_seqs - 1} with at least one token each are needed, got {seqs}")
+        lens[seqs] = [len(t) for t in toks]
+        n = int(lens.sum())
+        if n > self.n_max:
+            raise ValueError(f"{n} new tokens, at most {self.n_max}")
+        st = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(st):
+            before = cache.ctx_len.clone()
+            status = cache.reserve(seqs, lens[seqs], stream=st)
+            if int(status.max().item()):
+                bad = [k for k, v in zip(seqs, status.tolist()) if v]
+                # what was granted is given back: lengths first, then the pages behind them
+                self._give_back(before, st)
+                raise I4Error(I4_ENOMEM, f"ChunkedDecoder.run: no pages for {lens[bad].tolist()} tokens of sequences {bad}")
+            start = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(dev)
+            last = torch.from_numpy((np.cumsum(lens[seqs]) - 1).astype(np.int32)).to(dev)
+            tokens = torch.from_numpy(np.concatenate(toks)).to(dev)
+            r, xn, qkv, q, attn, y, gu, mlp = (t[:n] for t in (self.r, self.xn, self.qkv, self.q, self.attn, self.y, self.gu,
+                                                               self.mlp))
+            flat, longest = attn.view(n, -1), int(lens.max())
+            embed_gather(g["embed"], tokens, r, stream=st)
+            rmsnorm(r, L[0]["ln_in"], out=xn, eps=s.eps, stream=st)
+            for li, lw in enumerate(L):
+                int4_gemm(lw["w_qkv"], lw["s_qkv"], xn, lw["b_qkv"], y=qkv, ws=self.gemm_ws, stream=st)
+                rope_append_chunk(qkv, start, cache.ctx_len, self.cs, s.n_q, s.n_kv, cache.k_pools[li], cache.v_pools[li],
+                                  cache.page_table, q_out=q, stream=st)
+                paged_gqa_chunk(q, cache.k_pools[li], cache.v_pools[li], cache.page_table, start, cache.ctx_len, out=attn,
+                                max_q=longest, ws=self.attn_ws, stream=st)
+                int4_gemm(lw["w_o"], lw["s_o"], flat, y=y, ws=self.gemm_ws, stream=st)
+                rmsnorm(y, lw["ln_post"], out=xn, resid=r, eps=s.eps, stream=st)
+                int4_gemm(lw["w_gu"], lw["s_gu"], xn, y=gu, ws=self.gemm_ws, stream=st)
+                silu_mul(gu, out=mlp, stream=st)
+                int4_gemm(lw["w_d"], lw["s_d"], mlp, y=y, ws=self.gemm_ws, stream=st)
+                gamma = L[li + 1]["ln_in"] if li + 1 < len(L) else g["ln_final"]
+                rmsnorm(y, gamma, out=xn, resid=r, eps=s.eps, stream=st)
+            ends = torch.empty((len(seqs), s.hidden), dtype=torch.float16, device=dev)
+            embed_gather(xn, last, ends, stream=st)
+            logits = int4_gemm(g["w_lm"], g["s_lm"], ends, out_fp32=True, ws=self.gemm_ws, stream=st)
+            out = torch.empty(len(seqs), dtype=torch.int32, device=dev)
+            argmax_rows(logits, out, stream=st)
+        return out, logits
+
+    def _give_back(self, before, st):
+        """After a reservation that was granted in part: the lengths as they were before, and the pages behind them free."""
+        import torch
+        cache, P = self.cache, self.cache.page_size
+        place = torch.arange(cache.max_pages, device=before.device)
+        held = lambda ctx: place < ((ctx + P - 1) // P)[:, None]  # noqa: E731
+        new = held(cache.ctx_len) & ~held(before)
+        cache.refs.index_put_((cache.page_table[new].long(),), torch.zeros((), dtype=torch.int32, device=before.device))
+        cache.page_table.masked_fill_(new, -1)
+        cache.ctx_len.copy_(before)
