@@ -53,6 +53,9 @@ struct Cfg {
     static constexpr int kUnitRows = NQ * kRows;
     static constexpr int kUnitCost = 2;  // what beginning and ending a unit costs, in tiles
     static constexpr int kMinCost = 2;   // tiles that are worth a CTA of their own
+    // rows of a warp of the joining kernel, out of eight loads in flight: the few rows of short chunks come in many parts
+    // (four single tokens: 16.0 us with 2, 16.8 with 4), full tiles in two or three (a mixed batch: 52.1 and 48.6 us)
+    static constexpr int kJoinRows = NQ == 2 ? 4 : 2;
     static constexpr int kWhole = 4;     // a unit of at most so many tiles is not cut: joining would take longer
     static constexpr unsigned kTmemCols = NQ * 256;  // S / P and O of every slot
     static constexpr unsigned kSmem = 1024 + (NQ + kStages) * kTileBytes;
@@ -629,13 +632,15 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 if (!ok) return;
                 fence_after_sync();
             }
+            const bool few = last_r.z * G <= 32;
+            const long long own = mine ? ((long long)(last.row0 + tok) * p.Hq + head) * 128 : -1;
             long long to[4];  // output rows of this group of four lanes, or -1
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                to[k] = __shfl_sync(0xffffffffu, mine ? ((long long)(last.row0 + tok) * p.Hq + head) * 128 : -1ll, (lane & ~3) + k);
+            for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, own, (lane & ~3) + k);
             float bad[4] = {0.f, 0.f, 0.f, 0.f};  // stay 0 while every value of O is finite
-#pragma unroll 2
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
+                if (few && wq > 0) break;  // no rows in this warp
                 uint32_t o[32];
                 if (any) {
                     tmem_ld32(tO + 32 * c, o);
@@ -646,6 +651,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) bad[i & 3] = fmaf(__uint_as_float(o[i]), 0.f, bad[i & 3]);
+                // Lanes that store their own rows touch 32 lines with every store; turned four by four, 8. Rows of one warp
+                // alone are stored as they are: turning costs that warp more (2.3 us against 1.2).
                 if (last.whole) {
                     uint4 v[4];  // 16-byte chunks 4c .. 4c + 3 of this lane's row
 #pragma unroll
@@ -657,10 +664,24 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                                                              __uint_as_float(o[8 * i + 2 * k + 1]) * l_inv));
                         v[i] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
-                    transpose4(v);  // now chunk 4c + (lane & 3) of the rows of this group of four lanes
+                    if (few) {
+                        if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (to[k] >= 0) *reinterpret_cast<uint4 *>(p.out + to[k] + 32 * c + 8 * (lane & 3)) = v[k];
+                            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(p.out + own + 32 * c + 8 * k) = v[k];
+                        }
+                    } else {
+                        transpose4(v);  // now chunk 4c + (lane & 3) of the rows of this group of four lanes
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (to[k] >= 0) *reinterpret_cast<uint4 *>(p.out + to[k] + 32 * c + 8 * (lane & 3)) = v[k];
+                    }
+                } else if (any && few) {
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(p.part_o + (size_t)slot_row * 128 + 32 * c + 4 * i) =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
                 } else if (any) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -799,8 +820,9 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 }
 
 // The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
-// Grid (CTAs of the main kernel, row blocks of 32); a warp has four rows, lane = four columns. The weights of 32 parts are in
+// Grid (CTAs of the main kernel, blocks of 32 rows); a warp has R rows at once, lane = four columns. The weights of 32 parts are in
 // the lanes at once and eight loads are in flight, so the kernel costs a few latencies (it is bound by nothing else).
+template <int R>
 __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
     const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x;
     grid_dep_wait();
@@ -808,8 +830,9 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
     if (!c.valid) return;
     const int parts = c.last - first + 2;
     const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
-    constexpr int R = 4;  // rows of a warp, all in flight together
-    const int row0 = blockIdx.y * 32 + R * (threadIdx.x >> 5);
+    constexpr int U = 8 / R;  // parts of each of a warp's R rows that are in flight together
+#pragma unroll 1
+    for (int row0 = blockIdx.y * 32 + R * (threadIdx.x >> 5); row0 < (int)blockIdx.y * 32 + 32; row0 += 8 * R) {
     bool in[R];
     float M[R], L[R];
     float4 o[R];
@@ -851,10 +874,10 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
         }
         const int n = min(32, parts - k0);
 #pragma unroll 1
-        for (int k1 = 0; k1 < n; k1 += 2) {
-            float4 v[2][R];
+        for (int k1 = 0; k1 < n; k1 += U) {
+            float4 v[U][R];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < U; ++k)
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -862,7 +885,7 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
                         v[k][i] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row0 + i) * 32 + lane];
                 }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < U; ++k)
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const float wk = __shfl_sync(0xffffffffu, w[i], k1 + k);
@@ -880,6 +903,7 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
         h.x = h2_bits(__floats2half2_rn(o[i].x * inv, o[i].y * inv));
         h.y = h2_bits(__floats2half2_rn(o[i].z * inv, o[i].w * inv));
         *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + c.g * G + row % kRows - in_slot * G) * 128 + 4 * lane) = h;
+    }
     }
 }
 
@@ -934,7 +958,7 @@ static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUte
     chunk_attn_kernel<NQ><<<grid, Cfg<NQ>::kThreads, Cfg<NQ>::kSmem, stream>>>(tq, tk, tv, p);
     int st = launch_check("i4_paged_gqa_chunk");
     if (st) return st;
-    return cuda_check(launch(chunk_join_kernel, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, true, p,
+    return cuda_check(launch(chunk_join_kernel<Cfg<NQ>::kJoinRows>, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, true, p,
                              (int)Cfg<NQ>::kUnitRows),
                       "i4_paged_gqa_chunk join");
 }
