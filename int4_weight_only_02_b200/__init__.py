@@ -16,6 +16,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libi4rt.so")
@@ -96,10 +97,10 @@ _SIGS = {
                                 _vp]),
     "i4_kv_pages_ws_bytes": (_sz, [_i, _i]),
     "i4_kv_pages_copy": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]),
-    "i4_kv_pages_reserve": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _vp, _i, _vp, _vp, _sz, _vp]),
-    "i4_kv_pages_fork": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
-    "i4_kv_pages_free": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _vp]),
-    "i4_kv_pages_compact": (_i, [ctypes.POINTER(KvCacheDesc), _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_reserve": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_fork": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "i4_kv_pages_free": (_i, [_vp, _vp, _i, _vp]),
+    "i4_kv_pages_compact": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "decode_step_graph_create": (_i, [ctypes.POINTER(ModelDesc), ctypes.POINTER(ModelWeights),
                                       ctypes.POINTER(SeqState), ctypes.POINTER(_vp)]),
     "decode_step_graph_replay": (_i, [_vp, _vp]),
@@ -327,21 +328,41 @@ def _refuse(name: str, what: str):
     raise I4Error(I4_EINVAL, f"{name}: {what}")
 
 
-def _tensors(name: str, *groups) -> int:
-    """Refuses tensors that the call could not follow: every (tensor, dtype, dims) has that type and number of
-    dimensions, is contiguous and lies on the current CUDA device (whose current stream the call uses). Returns the
-    device's index. The calls below take microseconds on the GPU, so what is asked of each tensor is kept cheap."""
+def _tensors(name: str, dims_of, f16=(), i32=(), other=()) -> int:
+    """Refuses tensors that the call could not follow: all are contiguous and lie on the current CUDA device (whose
+    current stream the call uses), those of ``f16`` and ``i32`` have that type and ``other`` is (tensor, dtype) pairs;
+    ``dims_of`` gives the numbers of dimensions in the same order. Returns the device's index. The calls take
+    microseconds on the GPU, so each tensor is asked four cheap questions."""
     import torch
-    for t, dtype, dims in groups:
+    dev = (f16 or i32)[0].get_device()
+    half, whole = torch.float16, torch.int32
+    ok = dev >= 0 and dev == torch.cuda.current_device()
+    i = 0
+    for t in f16:
+        ok = ok and t.dtype is half and t.dim() == dims_of[i] and t.is_contiguous() and t.get_device() == dev
+        i += 1
+    for t in i32:
+        ok = ok and t.dtype is whole and t.dim() == dims_of[i] and t.is_contiguous() and t.get_device() == dev
+        i += 1
+    for t, dtype in other:
+        ok = ok and t.dtype is dtype and t.dim() == dims_of[i] and t.is_contiguous() and t.get_device() == dev
+        i += 1
+    if ok:
+        return dev
+    every = [(t, half) for t in f16] + [(t, whole) for t in i32] + list(other)
+    for (t, dtype), dims in zip(every, dims_of):
         if t.dtype is not dtype or t.dim() != dims or not t.is_contiguous():
             _refuse(name, f"a contiguous {dtype} tensor of {dims} dimensions is needed, got {t.dtype} {tuple(t.shape)}")
-    dev = groups[0][0].get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        _refuse(name, f"tensors on the current CUDA device are needed, got {groups[0][0].device}")
-    for t, _, _ in groups:
-        if t.get_device() != dev:
-            _refuse(name, f"tensors on cuda:{dev} and {t.device}")
-    return dev
+    _refuse(name, f"tensors on the current CUDA device are needed, got {sorted({str(t.device) for t, _ in every})}")
+
+
+def _alloc(stream, make, *args, **kw):
+    """make(*args, **kw) on the call's stream: what a call allocates for itself is filled, used and given back there."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -363,7 +384,7 @@ def rope_table(max_pos: int, rotary_dim: int = 128, theta: float = 1e6, scaling:
     import torch
     if scaling not in ROPE_SCALINGS:
         _refuse("rope_table", f"scaling {scaling!r} is none of {sorted(ROPE_SCALINGS)}")
-    cs = torch.empty((max(int(max_pos), 0), max(int(rotary_dim), 0) // 2, 2), dtype=torch.float32, device=device)
+    cs = _alloc(stream, torch.empty, (max(int(max_pos), 0), max(int(rotary_dim), 0) // 2, 2), dtype=torch.float32, device=device)
     if cs.device.type != "cuda" or cs.device.index != torch.cuda.current_device():
         _refuse("rope_table", f"the current CUDA device is needed, got {cs.device}")
     _check(lib().i4_rope_table(_p(cs), int(max_pos), int(rotary_dim), float(theta), ROPE_SCALINGS[scaling],
@@ -378,15 +399,15 @@ def rope_append_chunk(qkv, q_start, ctx_len, cs, Hq: int, Hkv: int, k_pool, v_po
     the pages. The rotated part of a head is cs.shape[1] * 2 values."""
     import torch
     name = "rope_append_chunk"
-    f16, i32 = torch.float16, torch.int32
+    f16 = torch.float16
     if qkv.dim() != 2 or qkv.dtype is not f16 or (qkv.stride(1) != 1 and qkv.shape[1] > 1):
         _refuse(name, "qkv [T][(Hq+2Hkv)*128] fp16 with adjacent columns is needed")
     T, width = qkv.shape
     B, max_pages = page_table.shape
     if q_out is None:
-        q_out = torch.zeros((T, Hq, 128), device=qkv.device, dtype=f16)
-    dev = _tensors(name, (q_start, i32, 1), (ctx_len, i32, 1), (cs, torch.float32, 3), (k_pool, f16, 4), (v_pool, f16, 4),
-                   (page_table, i32, 2), (q_out, f16, 3))
+        q_out = _alloc(stream, torch.zeros, (T, Hq, 128), device=qkv.device, dtype=f16)
+    dev = _tensors(name, (4, 4, 3, 1, 1, 2, 3), (k_pool, v_pool, q_out), (q_start, ctx_len, page_table),
+                   ((cs, torch.float32),))
     num_pages, hkv, P, D = shape = k_pool.shape
     max_pos, half, two = cs.shape
     if (qkv.get_device() != dev or width != (Hq + 2 * Hkv) * D or hkv != Hkv or v_pool.shape != shape
@@ -414,17 +435,16 @@ def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, w
     allocated when not given. Rows behind the last sequence are left alone (zeros in an ``out`` made here)."""
     import torch
     name = "paged_gqa_chunk"
-    f16, i32 = torch.float16, torch.int32
+    f16 = torch.float16
     if q.dim() != 3 or q.dtype is not f16 or q.stride(2) != 1 or (q.stride(1) != q.shape[2] and q.shape[1] > 1):
         _refuse(name, "q [T][Hq][128] fp16 with adjacent heads is needed")
     T, Hq, D = shape = q.shape
     B, max_pages = page_table.shape
     if out is None:
-        out = torch.zeros((T, Hq, D), device=q.device, dtype=f16)
+        out = _alloc(stream, torch.zeros, (T, Hq, D), device=q.device, dtype=f16)
     if ws is None:
-        ws = torch.empty(paged_gqa_chunk_ws_bytes(), device=q.device, dtype=torch.uint8)
-    dev = _tensors(name, (k_pool, f16, 4), (v_pool, f16, 4), (page_table, i32, 2), (q_start, i32, 1), (ctx_len, i32, 1),
-                   (out, f16, 3), (ws, torch.uint8, 1))
+        ws = _alloc(stream, torch.empty, paged_gqa_chunk_ws_bytes(), device=q.device, dtype=torch.uint8)
+    dev = _tensors(name, (4, 4, 3, 2, 1, 1, 1), (k_pool, v_pool, out), (page_table, q_start, ctx_len), ((ws, torch.uint8),))
     num_pages, Hkv, P, dk = pool = k_pool.shape
     if (q.get_device() != dev or dk != D or v_pool.shape != pool or out.shape != shape or q_start.numel() != B + 1
             or ctx_len.numel() != B):
@@ -459,39 +479,35 @@ def _pool_array(name: str, pools):
 def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, ws, *lists):
     """(the cache's descriptor, its device)."""
     import torch
-    i32 = torch.int32
-    groups = [(page_table, i32, 2), (ctx_len, i32, 1), (refs, i32, 1)]
-    if ws is not None:
-        groups.append((ws, torch.uint8, 1))
     n = lists[0].numel()
-    for t in lists:
-        groups.append((t, i32, 1))
-        if t.numel() != n:
-            _refuse(name, f"lists of different lengths: {[t.numel() for t in lists]}")
-    dev = _tensors(name, *groups)
+    dev = _tensors(name, _CACHE_DIMS, (), (page_table, ctx_len, refs, *lists), () if ws is None else ((ws, torch.uint8),))
     S, width = page_table.shape
-    if ctx_len.numel() != S:
-        _refuse(name, f"shapes do not match: page_table {tuple(page_table.shape)}, ctx_len {tuple(ctx_len.shape)}")
-    return KvCacheDesc(page_table.data_ptr(), ctx_len.data_ptr(), refs.data_ptr(), S, width, page_size, refs.numel()), dev
+    if ctx_len.numel() != S or any([t.numel() != n for t in lists]):
+        _refuse(name, f"shapes do not match: page_table {tuple(page_table.shape)}, ctx_len {tuple(ctx_len.shape)}, lists of "
+                      f"{[t.numel() for t in lists]}")
+    return _CACHE.pack(page_table.data_ptr(), ctx_len.data_ptr(), refs.data_ptr(), S, width, page_size, refs.numel()), dev
+
+
+_CACHE_DIMS = (2, 1, 1, 1, 1, 1, 1)  # page_table, then lists and the workspace
+_CACHE = struct.Struct("@3Q4i")  # i4_kv_cache (KvCacheDesc), packed in a quarter of a ctypes structure's time
 
 
 def kv_pages_ws_bytes(num_pages: int, n_seqs: int) -> int:
     return int(lib().i4_kv_pages_ws_bytes(num_pages, n_seqs))
 
 
-def _kv_ws(ws, page_table, refs):
+def _kv_ws(ws, page_table, refs, stream):
     import torch
     if ws is None:
-        ws = torch.empty(max(kv_pages_ws_bytes(refs.numel(), page_table.shape[0]), 256), dtype=torch.uint8,
+        ws = _alloc(stream, torch.empty, max(kv_pages_ws_bytes(refs.numel(), page_table.shape[0]), 256), dtype=torch.uint8,
                          device=refs.device)
     return ws
 
 
 def kv_pages_copy(pools, src, dst, stream=None):
     """Page src[i] -> dst[i] in every pool (device int32 lists; no page may be both source and target)."""
-    import torch
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_copy", pools)
-    dev = _tensors("kv_pages_copy", (src, torch.int32, 1), (dst, torch.int32, 1))
+    dev = _tensors("kv_pages_copy", (1, 1), (), (src, dst))
     if src.numel() != dst.numel():
         _refuse("kv_pages_copy", f"{src.numel()} sources and {dst.numel()} targets")
     _check(lib().i4_kv_pages_copy(arr.buffer_info()[0], len(pools), num_pages, Hkv, P, D, src.data_ptr(), dst.data_ptr(), src.numel(),
@@ -503,10 +519,10 @@ def kv_pages_reserve(page_table, ctx_len, refs, page_size: int, seqs, add, statu
     (0 done, 1 not enough free pages, 2 refused)."""
     import torch
     if status is None:
-        status = torch.empty_like(seqs)
-    ws = _kv_ws(ws, page_table, refs)
+        status = _alloc(stream, torch.empty_like, seqs)
+    ws = _kv_ws(ws, page_table, refs, stream)
     desc, dev = _cache_desc("kv_pages_reserve", page_table, ctx_len, refs, page_size, ws, seqs, add, status)
-    _check(lib().i4_kv_pages_reserve(ctypes.byref(desc), seqs.data_ptr(), add.data_ptr(), seqs.numel(), status.data_ptr(),
+    _check(lib().i4_kv_pages_reserve(desc, seqs.data_ptr(), add.data_ptr(), seqs.numel(), status.data_ptr(),
                                      ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "kv_pages_reserve")
     return status
 
@@ -517,12 +533,12 @@ def kv_pages_fork(pools, page_table, ctx_len, refs, src, dst, status=None, ws=No
     import torch
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_fork", pools)
     if status is None:
-        status = torch.empty_like(src)
-    ws = _kv_ws(ws, page_table, refs)
+        status = _alloc(stream, torch.empty_like, src)
+    ws = _kv_ws(ws, page_table, refs, stream)
     desc, dev = _cache_desc("kv_pages_fork", page_table, ctx_len, refs, P, ws, src, dst, status)
     if refs.numel() != num_pages:
         _refuse("kv_pages_fork", f"{refs.numel()} reference counts for {num_pages} pages")
-    _check(lib().i4_kv_pages_fork(ctypes.byref(desc), arr.buffer_info()[0], len(pools), Hkv, D, src.data_ptr(), dst.data_ptr(), src.numel(),
+    _check(lib().i4_kv_pages_fork(desc, arr.buffer_info()[0], len(pools), Hkv, D, src.data_ptr(), dst.data_ptr(), src.numel(),
                                   status.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "kv_pages_fork")
     return status
 
@@ -530,7 +546,7 @@ def kv_pages_fork(pools, page_table, ctx_len, refs, src, dst, status=None, ws=No
 def kv_pages_free(page_table, ctx_len, refs, page_size: int, seqs, stream=None):
     """The pages of the sequences are given back; their rows become -1 and their ctx_len 0."""
     desc, dev = _cache_desc("kv_pages_free", page_table, ctx_len, refs, page_size, None, seqs)
-    _check(lib().i4_kv_pages_free(ctypes.byref(desc), seqs.data_ptr(), seqs.numel(), _raw_stream(stream, dev)),
+    _check(lib().i4_kv_pages_free(desc, seqs.data_ptr(), seqs.numel(), _raw_stream(stream, dev)),
            "kv_pages_free")
 
 
@@ -540,12 +556,12 @@ def kv_pages_compact(pools, page_table, ctx_len, refs, n_live=None, ws=None, str
     import torch
     arr, (num_pages, Hkv, P, D) = _pool_array("kv_pages_compact", pools)
     if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    ws = _kv_ws(ws, page_table, refs)
+        n_live = _alloc(stream, torch.empty, 1, dtype=torch.int32, device=refs.device)
+    ws = _kv_ws(ws, page_table, refs, stream)
     desc, dev = _cache_desc("kv_pages_compact", page_table, ctx_len, refs, P, ws, n_live)
     if refs.numel() != num_pages or n_live.numel() != 1:
         _refuse("kv_pages_compact", f"{refs.numel()} reference counts for {num_pages} pages, n_live of {n_live.numel()}")
-    _check(lib().i4_kv_pages_compact(ctypes.byref(desc), arr.buffer_info()[0], len(pools), Hkv, D, n_live.data_ptr(), ws.data_ptr(),
+    _check(lib().i4_kv_pages_compact(desc, arr.buffer_info()[0], len(pools), Hkv, D, n_live.data_ptr(), ws.data_ptr(),
                                      ws.numel(), _raw_stream(stream, dev)), "kv_pages_compact")
     return n_live
 

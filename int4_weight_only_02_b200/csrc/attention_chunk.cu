@@ -10,23 +10,29 @@
 //    consecutive tokens, every K/V tile is read once for all of them, and a short chunk fills the rows better than one head's
 //    tokens would. One TMA box of (64 dims, G heads, 128 / G tokens) brings half of a slot's Q in that order.
 //  * Work. A unit is NQ slots' tokens of one sequence and one kv head; its cost is the
-//    number of 128-position tiles that its rows see. The units stand in one line (kv heads
-//    outermost) and every CTA, one or two per SM, takes an equal stretch of the line's tiles, whatever
-//    unit borders lie in it: a prompt's long and short units balance, and a
-//    single token's long context spreads over the GPU. A unit that is cut
-//    leaves its parts (m, l, O) in the workspace and a second kernel joins them in order.
-//    The lengths are read on the device: every CTA finds its stretch by itself with two block-wide scans.
+//    number of 128-position tiles that its rows see, and kUnitCost for beginning and ending it. The units stand in one line (kv
+//    heads outermost) and every CTA, one or two per SM, takes an equal stretch of the line: a prompt's long and short units
+//    balance, and a single token's long context spreads over the GPU. A unit that a border cuts leaves its parts
+//    (m, l, O) in the workspace and a second kernel joins them in order; a unit of at most kWhole tiles is not cut, since
+//    joining costs as much. The lengths are read on the device: every CTA finds its stretch by itself with two block-wide scans.
 //  * Data. One warp loads K and V tiles (32 KB) page by page with TMA into a ring, 128-byte
 //    swizzled; a page outside the pools, or one that no row sees, is an
 //    out-of-range coordinate, which fills zeros.
-//  * Math. S = Q K^T (M = 128 rows, N = 128 positions, both operands K-major in
-//    shared memory) into tensor memory; the 128 threads of a warpgroup own one row
-//    each, so maximum and sum need no exchange; P = 2^(S - m), rounded to fp16 (the tensor cores' operand
-//    type; 2^-11 of each weight), goes back over S's columns and is the A operand of O += P V (V MN-major). m only
-//    follows the row's maximum when that is more than 2^8 ahead, so O is rarely rescaled: P then reaches
-//    at most 2^8, far inside fp16. l and O are fp32.
-//  * Overlap. With NQ = 2 two warpgroups hold 128 rows each and alternate: the tensor cores
-//    run one's P V and next Q K^T while the other computes its exponentials. With NQ = 1 two CTAs share an SM.
+//  * Math. S = Q K^T (M = 128 rows, both operands K-major in shared memory) into tensor memory; the 128 threads of a
+//    warpgroup own one row each, so maximum and sum need no exchange; P = 2^(S - m), rounded to fp16 (the tensor cores'
+//    operand type; 2^-11 of each weight), goes back over S's columns and is the A operand of O += P V (V MN-major). m only
+//    follows the row's maximum when that is more than 2^8 ahead, so O is rarely rescaled (always following costs 20 %): P
+//    then reaches at most 2^8, far inside fp16. l and O are fp32.
+//  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
+//    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile and an SM; with
+//    NQ = 1, for chunks that fit one slot, two CTAs share an SM. (Whole tiles of 128 with the slots taking turns come out the same,
+//    254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.)
+//
+// Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows costs
+// 3072 cycles of 3300 measured, and under a steady load the GPU's power limit holds the clock near 1.6 GHz. 512 tokens behind 32768 positions
+// (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt
+// of 8192: 425 and 494 us. Few rows are bound by the chain of dependent steps: four single tokens at up to 2049 positions take 16 us,
+// 3.5 to the first tile (lengths, scans, first loads), 2 a tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.
 #include <cmath>
 
 #include "chunk.cuh"
@@ -365,26 +371,41 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 }
 
 // The sum over the positions [lo, hi) of one row by plain loads, for rows whose tensor-core sum met a NaN or an
-// infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. Lane: dims 4 lane ..
-// 4 lane + 3. The row's m and l are right already.
+// infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. The row's m and l are
+// right already. A lane has the score of one position of 32, then four dims of the sum over them (some 25 cycles a position, so
+// that a row of 2^20 positions stays far inside the other warps' waits).
 __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g, const uint16_t *q, int lo, int hi, float qs,
                                          float m_scaled) {
     const int lane = threadIdx.x & 31;
-    float o[4] = {0.f, 0.f, 0.f, 0.f}, x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = half_bits_to_float(q[4 * lane + i]);
-    for (int u = lo; u < hi; ++u) {
-        const int page = p.page_table[(size_t)b * p.max_pages + u / p.page_size];
-        if (page < 0 || page >= p.num_pages) continue;  // zeros
-        const size_t off = (((size_t)page * p.Hkv + g) * p.page_size + u % p.page_size) * 128 + 4 * lane;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u0 = lo; u0 < hi; u0 += 32) {
+        const int u = u0 + lane;
+        const int page = u < hi ? p.page_table[(size_t)b * p.max_pages + u / p.page_size] : -1;
+        const bool there = page >= 0 && page < p.num_pages;  // else K and V are zeros
+        const size_t off = there ? (((size_t)page * p.Hkv + g) * p.page_size + u % p.page_size) * 128 : 0;
         float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fmaf(x[i], half_bits_to_float(p.k_pool[off + i]), s);
-        const float w = ex2(fmaf(warp_sum(s), qs, -m_scaled));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = fmaf(w, half_bits_to_float(p.v_pool[off + i]), o[i]);
+        if (there)
+            for (int c = 0; c < 128; c += 8) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(p.k_pool + off + c), x = *reinterpret_cast<const uint4 *>(q + c);
+                s = fma2_f16_f32(a.x, x.x, s);
+                s = fma2_f16_f32(a.y, x.y, s);
+                s = fma2_f16_f32(a.z, x.z, s);
+                s = fma2_f16_f32(a.w, x.w, s);
+            }
+        const float w = ex2(fmaf(s, qs, -m_scaled));
+        const unsigned rows = __ballot_sync(0xffffffffu, there);
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)off, k);
+            if (!((rows >> k) & 1)) continue;
+            const uint2 v = *reinterpret_cast<const uint2 *>(p.v_pool + at + 4 * lane);
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+            const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+            o = make_float4(fmaf(wk, a.x, o.x), fmaf(wk, a.y, o.y), fmaf(wk, c.x, o.z), fmaf(wk, c.y, o.w));
+        }
     }
-    return make_float4(o[0], o[1], o[2], o[3]);
+    return o;
 }
 
 template <int NQ>
@@ -1003,6 +1024,9 @@ extern "C" int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const u
         return fail(I4_EUNSUPPORTED, "i4_paged_gqa_chunk: page_size %d must be a power of two in [8, 128]", page_size);
     if (T > (1 << 20) || B > 65536 || Hkv > 4096 || (long long)max_pages_per_seq * page_size > (1 << 20))
         return fail(I4_EUNSUPPORTED, "i4_paged_gqa_chunk: more than 2^20 tokens, 65536 sequences or 4096 kv heads");
+    // a CTA's share of the line of tiles is counted in 31 bits
+    if ((double)Hkv * (T / (kRows / (Hq / Hkv)) + (double)B) * ((double)max_pages_per_seq * page_size / kTile + 3) > 1e11)
+        return fail(I4_EUNSUPPORTED, "i4_paged_gqa_chunk: T, B, Hkv and the page-table row are too large together");
     if (!(scale > 0.f) || std::isinf(scale)) return fail(I4_EINVAL, "i4_paged_gqa_chunk: scale %g must be positive", scale);
     if (q_stride < (long long)Hq * D || q_stride % 8)
         return fail(I4_EINVAL, "i4_paged_gqa_chunk: q_stride %lld must be >= Hq*D and a multiple of 8", q_stride);
@@ -1019,7 +1043,7 @@ extern "C" int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const u
     CUtensorMap tq, tk, tv;
     // q as [T][Hq][128] in boxes of one kv head's rows of a slot's tokens; the pools as [pages][Hkv][P][128] in boxes of a page
     const cuuint64_t page = 256ull * page_size, tok = 2ull * (cuuint64_t)q_stride;
-    const cuuint64_t qd[4] = {128, (cuuint64_t)Hq, (cuuint64_t)T, 1}, qs[3] = {256, tok, tok * (cuuint64_t)T};
+    const cuuint64_t qd[4] = {128, (cuuint64_t)Hq, (cuuint64_t)T, 1}, qs[3] = {256, tok, tok};
     const cuuint64_t pd[4] = {128, (cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)num_pages}, ps[3] = {256, page, page * Hkv};
     const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G), 1}, pb[4] = {64, (cuuint32_t)page_size, 1, 1};
     if ((st = row_map(&tq, q, qd, qs, qb)) || (st = row_map(&tk, k_pool, pd, ps, pb)) || (st = row_map(&tv, v_pool, pd, ps, pb))) return st;

@@ -26,6 +26,7 @@ ATTN = [("q", FAKE), ("q_stride", 28 * 128), ("k", FAKE), ("v", FAKE), ("table",
     (dict(B=65537), -3), (dict(max_pages=1 << 17), -3), (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=float("nan")), -1),
     (dict(scale=float("inf")), -1), (dict(q_stride=28 * 128 - 8), -1), (dict(q_stride=28 * 128 + 4), -1), (dict(q=FAKE + 8), -2),
     (dict(k=FAKE + 8), -2), (dict(v=FAKE + 2), -2), (dict(out=FAKE + 8), -2), (dict(table=FAKE + 2), -2), (dict(q_start=FAKE + 1), -2),
+    (dict(T=1 << 20, B=65536, Hkv=4096, Hq=4096, q_stride=4096 * 128, max_pages=1 << 16, ws_bytes=1 << 40), -3),
     (dict(ws=None), -1), (dict(), -1), (dict(ws_bytes=1 << 40, ws=FAKE + 16), -2),
 ])
 def test_attention(i4lib, change, want):

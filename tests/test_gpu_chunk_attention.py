@@ -243,3 +243,82 @@ def test_same_as_the_decode_kernel(i4lib, cuda):
     ref = i4lib.paged_gqa_decode(dev(q, cuda), *clean, dev(np.maximum(table, 0), cuda), ctx).cpu().numpy()
     _, bound = cc.attention(q, k, v, table, lens, 16)
     assert np.all(np.abs(got.astype(np.float64) - ref) <= 2 * bound)
+
+
+def test_calls_that_allocate_on_another_stream(i4lib, cuda):
+    """Output and workspace made by the call, on a stream that is not the current one, while the current one keeps
+    allocating and overwriting what is given back."""
+    import torch
+    lens = [(1, 4000), (90, 90)]
+    q, k, v, table = case(lens, 7, 1, 16, seed=40)
+    args = [dev(a, cuda) for a in (q, k, v, table, cc.starts(lens), np.array([c for _, c in lens], dtype=np.int32))]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        outs.append(i4lib.paged_gqa_chunk(*args, stream=side))
+        for _ in range(3):
+            torch.full((i4lib.paged_gqa_chunk_ws_bytes() // 4,), float("nan"), device=cuda)
+    torch.cuda.synchronize()
+    for out in outs:
+        check(out.cpu().numpy(), q, k, v, table, lens, 16)
+
+
+def gpu_reference(q, k, v, scale=None):
+    """64-bit attention of rows q [Hq][128] over k, v [ctx][128] on the GPU, and the bound of cc.attention."""
+    import torch
+    scale = 1 / np.sqrt(cc.D) if scale is None else scale
+    qd, kd, vd = q.double(), k.double(), v.double()
+    p = torch.softmax(qd @ kd.T * scale, dim=1)
+    out, a = p @ vd, p @ vd.abs()
+    e = 128 * 2.0 ** -23 * scale * (qd.abs() @ kd.abs().T).amax(dim=1, keepdim=True)
+    bound = 2.0 ** -11 * (a + out.abs()) + 2 * e * a + 2.0 ** -13 * a + 2.0 ** -25 * (vd.abs().sum(0) + 1)
+    return out, bound
+
+
+def test_a_million_positions(i4lib, cuda):
+    """The longest row of the page table. A row's sums pass 8192 tiles instead of the 2^9 additions of cc.attention's
+    bound: 2^-23 * 8192 * A = 2^-10 A more."""
+    import torch
+    ctx, page = 1 << 20, 128
+    gen = torch.Generator(device=cuda).manual_seed(1)
+    k, v = (torch.randn((ctx // page, 1, page, 128), generator=gen, device=cuda, dtype=torch.float16) for _ in range(2))
+    q = torch.randn((2, 4, 128), generator=gen, device=cuda, dtype=torch.float16)
+    perm = torch.randperm(ctx // page, generator=gen, device=cuda)
+    table = perm.to(torch.int32)[None].contiguous()
+    start, n = torch.tensor([0, 2], dtype=torch.int32, device=cuda), torch.tensor([ctx], dtype=torch.int32, device=cuda)
+    got = i4lib.paged_gqa_chunk(q, k, v, table, start, n, max_q=2)
+    kk, vv = (t[perm][:, 0].reshape(-1, 128) for t in (k, v))
+    for i in range(2):
+        want, bound = gpu_reference(q[i], kk[:ctx - 1 + i], vv[:ctx - 1 + i])
+        a = (bound / 2.0 ** -11).abs()  # at least A
+        assert bool(((got[i].double() - want).abs() <= bound + 2.0 ** -10 * a).all())
+    assert i4lib.device_error() == 0
+
+
+def test_pools_behind_32_bits(i4lib, cuda):
+    """Pages whose values lie more than 2^32 bytes and 2^31 values into the pools: attention, append and copy."""
+    import torch
+    pages, page = (1 << 31) // (2 * 128 * 128) + 70, 128
+    f16, i32 = torch.float16, torch.int32
+    k, v = (torch.empty((pages, 2, page, 128), dtype=f16, device=cuda) for _ in range(2))
+    assert k.numel() > 1 << 31
+    gen = torch.Generator(device=cuda).manual_seed(2)
+    ids = [pages - 1, 3, pages - 60, pages - 2]
+    for t in (k, v):
+        t[ids] = torch.randn((4, 2, page, 128), generator=gen, device=cuda, dtype=f16)
+    q = torch.randn((3, 4, 128), generator=gen, device=cuda, dtype=f16)
+    table = torch.tensor([ids], dtype=i32, device=cuda)
+    start, n = torch.tensor([0, 3], dtype=i32, device=cuda), torch.tensor([500], dtype=i32, device=cuda)
+    cs = i4lib.rope_table(512, 128)
+    qkv = torch.randn((3, 8 * 128), generator=gen, device=cuda, dtype=f16)
+    i4lib.rope_append_chunk(qkv, start, n, cs, 4, 2, k, v, table)
+    assert torch.equal(v[pages - 2, :, 113:116].transpose(0, 1).reshape(3, -1), qkv[:, 6 * 128:])
+    got = i4lib.paged_gqa_chunk(q, k, v, table, start, n)
+    for i in range(3):
+        for h in range(4):
+            kk, vv = (t[ids, h // 2].reshape(-1, 128)[:498 + i] for t in (k, v))
+            want, bound = gpu_reference(q[i, h:h + 1], kk, vv)
+            assert bool(((got[i, h].double() - want[0]).abs() <= bound[0]).all())
+    i4lib.kv_pages_copy([k, v], table[0, :1].contiguous(), torch.tensor([pages - 70], dtype=i32, device=cuda))
+    assert torch.equal(k[pages - 70], k[pages - 1]) and torch.equal(v[pages - 70], v[pages - 1])
