@@ -344,63 +344,64 @@ __device__ __forceinline__ void copy_span(unsigned char *dst, const unsigned cha
         if (v0 + u * kCopyThreads < vecs) __stcs(reinterpret_cast<uint4 *>(dst) + v0 + u * kCopyThreads, v[u]);
 }
 
-// Whole pages src[i] -> dst[i] of every pool; n_dev, when given, is the device's count. Work item: (pool, i, part). The first
-// remap_blocks blocks instead give table entries of held pages at or above n_live (n_dev[1]) the page's new id.
-__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ PoolPtrs pools, int n_pools, const int32_t *src,
+// Whole pages src[i] -> dst[i] of pool blockIdx.y; n_dev, when given, is the device's count. Work item: (i, part of the page). The
+// first remap_blocks blocks of a row of the grid instead give table entries of held pages at or above n_live (n_dev[1])
+// the page's new id. Bound by HBM: 300 pages of 56 pools (551 MB) in 83 us, 6.6 TB/s.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ PoolPtrs pools, const int32_t *src,
                                                                const int32_t *dst, int n, const int32_t *n_dev, int num_pages,
                                                                int page_vecs, int parts, const CacheArgs c, const int32_t *new_id,
                                                                int remap_blocks) {
     grid_dep_wait();
     if ((int)blockIdx.x < remap_blocks) {
         const int n_live = n_dev[1];
-        const long long entries = (long long)c.S * c.max_pages;
-        for (long long x = blockIdx.x * (long long)kCopyThreads + threadIdx.x; x < entries; x += (long long)remap_blocks * kCopyThreads) {
+        const long long entries = (long long)c.S * c.max_pages, step = (long long)remap_blocks * gridDim.y * kCopyThreads;
+        for (long long x = (blockIdx.x * (long long)gridDim.y + blockIdx.y) * kCopyThreads + threadIdx.x; x < entries; x += step) {
             const int s = (int)(x / c.max_pages), j = (int)(x % c.max_pages), p = c.table[x];
             if (j < pages_of(c.ctx_len[s], c.P, c.max_pages) && p >= n_live && p < c.num_pages) c.table[x] = new_id[p];
         }
         return;
     }
     if (n_dev) n = min(n, *n_dev);
-    const long long items = (long long)n_pools * n * parts;
-    for (long long it = blockIdx.x - remap_blocks; it < items; it += gridDim.x - remap_blocks) {
-        const int part = (int)(it % parts);
-        const long long r = it / parts;
-        const int i = (int)(r % n), pool = (int)(r / n);
+    unsigned char *pool = pools.p[blockIdx.y];
+    const unsigned items = (unsigned)n * (unsigned)parts;
+    for (unsigned it = blockIdx.x - remap_blocks; it < items; it += gridDim.x - remap_blocks) {
+        const unsigned i = it / (unsigned)parts;
         const int from = src[i], to = dst[i];
         if (from < 0 || from >= num_pages || to < 0 || to >= num_pages || from == to) continue;
-        copy_span(pools.p[pool] + (size_t)to * page_vecs * 16, pools.p[pool] + (size_t)from * page_vecs * 16, page_vecs, part);
+        copy_span(pool + (size_t)to * page_vecs * 16, pool + (size_t)from * page_vecs * 16, page_vecs, (int)(it - i * parts));
     }
 }
 
-// The first `fill` rows of every head of page from[i] -> page to[i] in every pool. Work item: (pool, i, part of the page);
-// the filled rows of the heads of a page are numbered one after the other.
-__global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid_constant__ PoolPtrs pools, int n_pools,
-                                                                    const int32_t *from, const int32_t *to, const int32_t *fill, int n,
-                                                                    int Hkv, int P, int row_vecs, int parts) {
+// The first `fill` rows of every head of page from[i] -> page to[i] in pool blockIdx.y. Work item: (i, part of the page); the
+// filled rows of the heads of a page are numbered one after the other, and a thread has kCopyUnroll of them in flight.
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid_constant__ PoolPtrs pools, const int32_t *from,
+                                                                    const int32_t *to, const int32_t *fill, int n, int Hkv, int P,
+                                                                    int row_vecs, int parts) {
     grid_dep_wait();
-    const long long items = (long long)n_pools * n * parts;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int part = (int)(it % parts);
-        const long long r = it / parts;
-        const int i = (int)(r % n), pool = (int)(r / n);
-        const int span = fill[i] * row_vecs;  // 16-byte vectors of one head
-        const int vecs = span * Hkv;
-        if (part * kCopyThreads * kCopyUnroll >= vecs) continue;
-        const uint4 *s = reinterpret_cast<const uint4 *>(pools.p[pool]) + (size_t)from[i] * Hkv * P * row_vecs;
-        uint4 *d = reinterpret_cast<uint4 *>(pools.p[pool]) + (size_t)to[i] * Hkv * P * row_vecs;
+    const unsigned items = (unsigned)n * (unsigned)parts;
+    for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
+        const unsigned i = it / (unsigned)parts;
+        const int span = fill[i] * row_vecs, vecs = span * Hkv;  // 16-byte vectors of one head, of all
+        int x = (int)(it - i * parts) * kCopyThreads * kCopyUnroll + threadIdx.x;
+        if (x - (int)threadIdx.x >= vecs) continue;
+        const uint4 *s = reinterpret_cast<const uint4 *>(pools.p[blockIdx.y]) + (size_t)from[i] * Hkv * P * row_vecs;
+        uint4 *d = reinterpret_cast<uint4 *>(pools.p[blockIdx.y]) + (size_t)to[i] * Hkv * P * row_vecs;
+        int head = x / span, in_head = x - head * span;
         uint4 v[kCopyUnroll];
-        size_t at[kCopyUnroll];
+        int at[kCopyUnroll];
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u) {
-            const int x = (part * kCopyUnroll + u) * kCopyThreads + threadIdx.x;
-            if (x < vecs) {
-                at[u] = (size_t)(x / span) * P * row_vecs + x % span;
-                v[u] = __ldcs(s + at[u]);
+            at[u] = head * P * row_vecs + in_head;
+            if (x + u * kCopyThreads < vecs) v[u] = __ldcg(s + at[u]);
+            in_head += kCopyThreads;
+            while (in_head >= span) {  // once at most where a head has 256 filled vectors
+                in_head -= span;
+                ++head;
             }
         }
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u)
-            if ((part * kCopyUnroll + u) * kCopyThreads + (int)threadIdx.x < vecs) __stcs(d + at[u], v[u]);
+            if (x + u * kCopyThreads < vecs) d[at[u]] = v[u];
     }
 }
 
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid
 static int check_pools(const char *what, void *const *pools, int n_pools, int num_pages, int Hkv, int P, int D) {
     if (!pools) return fail(I4_EINVAL, "%s: null pointer", what);
     if (n_pools < 1 || num_pages < 1 || num_pages > kMaxPages || Hkv < 1 || P < 1 || D < 8 || D % 8 ||
-        (long long)Hkv * P * D > (1 << 24))
+        (long long)Hkv * P * D > (1 << 22))
         return fail(I4_EINVAL, "%s: bad sizes (pools %d, pages %d, Hkv %d, page_size %d, D %d)", what, n_pools, num_pages, Hkv, P,
                     D);
     for (int i = 0; i < n_pools; ++i) {
@@ -461,9 +462,10 @@ static int plan_smem(K kernel, size_t bytes, const char *what) {
     return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what);
 }
 
-static int copy_grid(long long items) {
-    const long long most = 32ll * kNumSMs;
-    return (int)(items < most ? (items > 0 ? items : 1) : most);
+// Blocks along x for `items` work items in each of m pools: enough for the whole GPU, and no more than there are items.
+static unsigned copy_grid(long long items, int m) {
+    const long long most = (32ll * kNumSMs + m - 1) / m;
+    return (unsigned)(items < most ? (items > 0 ? items : 1) : most);
 }
 
 static int launch_copy(void *const *pools, int n_pools, const int32_t *src, const int32_t *dst, int n, const int32_t *n_dev,
@@ -476,11 +478,11 @@ static int launch_copy(void *const *pools, int n_pools, const int32_t *src, cons
         for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
         int blocks = 0;
         if (remap && p0 == 0) {
-            const long long b = ((long long)remap->S * remap->max_pages + kCopyThreads - 1) / kCopyThreads;
-            blocks = (int)(b < kNumSMs ? b : kNumSMs);
+            const long long b = ((long long)remap->S * remap->max_pages + kCopyThreads - 1) / kCopyThreads, rows = (b + m - 1) / m;
+            blocks = (int)(rows < 8 ? rows : 8);
         }
-        const int st = cuda_check(launch(kv_copy_kernel, dim3(blocks + copy_grid((long long)m * n * parts)), dim3(kCopyThreads), 0, stream,
-                                         n_dev != nullptr && p0 == 0, pp, m, src, dst, n, n_dev, num_pages, vecs, parts,
+        const int st = cuda_check(launch(kv_copy_kernel, dim3(blocks + copy_grid((long long)n * parts, m), m), dim3(kCopyThreads), 0, stream,
+                                         n_dev != nullptr && p0 == 0, pp, src, dst, n, n_dev, num_pages, vecs, parts,
                                          remap ? *remap : CacheArgs{}, new_id, blocks),
                                   what);
         if (st) return st;
@@ -544,8 +546,8 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
         PoolPtrs pp;
         const int m = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
-        st = cuda_check(launch(kv_copy_rows_kernel, dim3(copy_grid((long long)m * n * parts)), dim3(kCopyThreads), 0, (cudaStream_t)stream,
-                               p0 == 0, pp, m, (const int32_t *)L.b, (const int32_t *)L.c, (const int32_t *)L.c + n, n, Hkv,
+        st = cuda_check(launch(kv_copy_rows_kernel, dim3(copy_grid((long long)n * parts, m), m), dim3(kCopyThreads), 0, (cudaStream_t)stream,
+                               p0 == 0, pp, (const int32_t *)L.b, (const int32_t *)L.c, (const int32_t *)L.c + n, n, Hkv,
                                cache->page_size, row_vecs, parts),
                         "i4_kv_pages_fork copy");
         if (st) return st;

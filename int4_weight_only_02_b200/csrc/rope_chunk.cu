@@ -33,6 +33,8 @@ __global__ void rope_chunk_table_kernel(float2 *cs, int max_pos, int half, const
     }
 }
 
+constexpr int kRopeHeads = 4;
+
 struct RopeChunkParams {
     const uint16_t *qkv;
     long long qkv_stride;
@@ -45,17 +47,18 @@ struct RopeChunkParams {
 // One CTA per token. Sixteen lanes take one head, eight values (16 bytes) each, and a lane's partner values come
 // from the lane rd/16 away by shuffles (half layout) or are its own neighbours (interleaved). The angles of a lane are
 // the same for every head, so they are read once. Bound by HBM for many tokens and by the chain of dependent loads
-// (sequence, position, page and angles) for few: the first two heads' values, which depend on none of it, are loaded first.
-template <bool kInterleaved>
+// (sequence, position, page and angles) for few: the first heads' values, which depend on none of it, are loaded first.
+// A thread takes kHeads heads at once; finding the token's place costs it as much as two or three of them.
+template <bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkParams p) {
     const int t = blockIdx.x;
     const int c = threadIdx.x & 15;  // 16-byte chunk of the head
     const int heads = p.Hq + 2 * p.Hkv, step = blockDim.x >> 4, h_first = threadIdx.x >> 4;
     const uint16_t *src = p.qkv + (size_t)t * p.qkv_stride + 8 * c;
-    uint4 v[2];
+    uint4 v[kHeads];
     auto load = [&](int h0) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kHeads; ++k) {
             v[k] = make_uint4(0, 0, 0, 0);
             if (h0 + k * step < heads) v[k] = __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(h0 + k * step) * 128));
         }
@@ -65,8 +68,9 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
     if (b >= p.B) return;  // a row behind the last sequence
     const int2 rows = chunk_rows(p.q_start, b, p.T);
     const int pos = max(p.ctx_len[b], 0) - rows.y + (t - rows.x);
-    if (t < rows.x || pos < 0 || pos >= p.max_pos || pos / p.page_size >= p.max_pages) return;
-    const int page = p.page_table[(size_t)b * p.max_pages + pos / p.page_size], slot = pos % p.page_size;
+    const int in_row = (int)((unsigned)pos / (unsigned)p.page_size), slot = pos - in_row * p.page_size;
+    if (t < rows.x || pos < 0 || pos >= p.max_pos || in_row >= p.max_pages) return;
+    const int page = p.page_table[(size_t)b * p.max_pages + in_row];
     const bool page_ok = page >= 0 && page < p.num_pages;
 
     const int h16 = p.rd / 16;           // chunks of one half of the rotated part
@@ -84,10 +88,10 @@ __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkP
         cs[i] = make_float2(a.x, a.y);
         cs[i + 1] = make_float2(a.z, a.w);
     }
-    for (int h0 = h_first; h0 - h_first < heads; h0 += 2 * step) {  // the same trips for every thread: the shuffles need whole warps
+    for (int h0 = h_first; h0 - h_first < heads; h0 += kHeads * step) {  // the same trips for every thread: the shuffles need whole warps
         if (h0 != h_first) load(h0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kHeads; ++k) {
         const int h = h0 + k * step;
         uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, y[4];
         if (kInterleaved) {
@@ -192,13 +196,13 @@ extern "C" int i4_rope_append_chunk(const uint16_t *qkv, long long qkv_stride, c
     const RopeChunkParams p = {qkv,    qkv_stride, q_start, ctx_len, page_table, reinterpret_cast<const float2 *>(cs),
                                q_out,  k_pool,     v_pool,  max_pos, T,          B,
                                Hq,     Hkv,        rotary_dim, page_size, max_pages_per_seq, num_pages};
-    // two heads per sixteen lanes, whole warps, at most 512 threads
-    int threads = 16 * ((Hq + 2 * Hkv + 1) / 2);
+    // four heads per sixteen lanes, whole warps, at most 512 threads
+    int threads = 16 * ((Hq + 2 * Hkv + kRopeHeads - 1) / kRopeHeads);
     threads = (threads + 31) / 32 * 32;
     threads = threads > 512 ? 512 : threads;
     if (interleaved)
-        rope_append_chunk_kernel<true><<<T, threads, 0, (cudaStream_t)stream>>>(p);
+        rope_append_chunk_kernel<true, kRopeHeads><<<T, threads, 0, (cudaStream_t)stream>>>(p);
     else
-        rope_append_chunk_kernel<false><<<T, threads, 0, (cudaStream_t)stream>>>(p);
+        rope_append_chunk_kernel<false, kRopeHeads><<<T, threads, 0, (cudaStream_t)stream>>>(p);
     return launch_check("i4_rope_append_chunk");
 }
