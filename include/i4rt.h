@@ -284,11 +284,18 @@ I4_API int i4_rope_table(float *cs, int max_pos, int rotary_dim, double theta, i
  * skipped (q_out keeps its row); one whose page id is outside [0, num_pages) writes q_out only.
  * Two tokens that name the same page slot leave either one's values there.
  */
-I4_API int i4_rope_append_chunk(const uint16_t *qkv, long long qkv_stride, const int32_t *q_start, const int32_t *ctx_len,
-                                const float *cs, int max_pos, int rotary_dim, int interleaved, int T, int B, int Hq,
-                                int Hkv, int D, uint16_t *q_out, uint16_t *k_pool, uint16_t *v_pool,
-                                const int32_t *page_table, int page_size, int max_pages_per_seq, int num_pages,
-                                void *stream);
+typedef struct i4_rope_chunk_args {
+    const uint16_t *qkv;
+    long long qkv_stride;
+    const int32_t *q_start, *ctx_len;
+    const float *cs;
+    uint16_t *q_out, *k_pool, *v_pool;
+    const int32_t *page_table;
+    int max_pos, rotary_dim, interleaved;
+    int T, B, Hq, Hkv, D, page_size, max_pages_per_seq, num_pages;
+} i4_rope_chunk_args;
+
+I4_API int i4_rope_append_chunk(const i4_rope_chunk_args *args, void *stream);
 
 /*
  * Attention of new tokens over the pages, which hold their own K/V already.
@@ -309,10 +316,19 @@ I4_API int i4_rope_append_chunk(const uint16_t *qkv, long long qkv_stride, const
  * [8, 128], scale > 0, T <= 2^20, B <= 65536, max_pages_per_seq * page_size <= 2^20.
  */
 I4_API size_t i4_paged_gqa_chunk_ws_bytes(void);
-I4_API int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
-                              const int32_t *page_table, const int32_t *q_start, const int32_t *ctx_len, uint16_t *out, int T,
-                              int B, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages, int window,
-                              int max_q, float scale, void *ws, size_t ws_bytes, void *stream);
+typedef struct i4_chunk_attn_args {
+    const uint16_t *q;
+    long long q_stride;
+    const uint16_t *k_pool, *v_pool;
+    const int32_t *page_table, *q_start, *ctx_len;
+    uint16_t *out;
+    void *ws;
+    size_t ws_bytes;
+    int T, B, Hq, Hkv, D, page_size, max_pages_per_seq, num_pages, window, max_q;
+    float scale;
+} i4_chunk_attn_args;
+
+I4_API int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream);
 
 /*
  * Pages of a cache. `pools` is a HOST array of n_pools device pointers, each
@@ -343,7 +359,7 @@ I4_API int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const uint1
  * refused entry changes nothing, except that a fork that finds no page leaves dst
  * empty. Of a reserve, the first request that does not fit and every later one
  * that needs a page get status 1.
- *   n <= n_seqs <= 16384; num_pages <= 2^20; ws: i4_kv_pages_ws_bytes(num_pages, n_seqs) bytes,
+ *   n <= n_seqs <= 16384; num_pages <= 2^20; Hkv * page_size * D <= 2^22; ws: i4_kv_pages_ws_bytes(num_pages, n_seqs) bytes,
  *   16-byte aligned, any contents. Calls that share ws or the cache's arrays must not overlap.
  */
 typedef struct i4_kv_cache {

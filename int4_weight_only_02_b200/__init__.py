@@ -62,6 +62,20 @@ class RmsnormRopeArgs(ctypes.Structure):
                 ("max_pages_per_seq", _i)]
 
 
+class RopeChunkArgs(ctypes.Structure):
+    _fields_ = [("qkv", _vp), ("qkv_stride", ctypes.c_longlong), ("q_start", _vp), ("ctx_len", _vp), ("cs", _vp),
+                ("q_out", _vp), ("k_pool", _vp), ("v_pool", _vp), ("page_table", _vp), ("max_pos", _i), ("rotary_dim", _i),
+                ("interleaved", _i), ("T", _i), ("B", _i), ("Hq", _i), ("Hkv", _i), ("D", _i), ("page_size", _i),
+                ("max_pages_per_seq", _i), ("num_pages", _i)]
+
+
+class ChunkAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_stride", ctypes.c_longlong), ("k_pool", _vp), ("v_pool", _vp), ("page_table", _vp),
+                ("q_start", _vp), ("ctx_len", _vp), ("out", _vp), ("ws", _vp), ("ws_bytes", _sz), ("T", _i), ("B", _i),
+                ("Hq", _i), ("Hkv", _i), ("D", _i), ("page_size", _i), ("max_pages_per_seq", _i), ("num_pages", _i),
+                ("window", _i), ("max_q", _i), ("scale", _f)]
+
+
 class KvCacheDesc(ctypes.Structure):
     _fields_ = [("page_table", _vp), ("ctx_len", _vp), ("refs", _vp), ("n_seqs", _i), ("max_pages_per_seq", _i),
                 ("page_size", _i), ("num_pages", _i)]
@@ -90,11 +104,9 @@ _SIGS = {
     "i4_rope_kv_append": (_i, [_vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _i, _vp]),
     "silu_mul": (_i, [_vp, _vp, _i, _i, _vp]),
     "i4_rope_table": (_i, [_vp, _i, _i, _d, _i, _d, _i, _vp]),
-    "i4_rope_append_chunk": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
-                                  _vp]),
+    "i4_rope_append_chunk": (_i, [_vp, _vp]),
     "i4_paged_gqa_chunk_ws_bytes": (_sz, []),
-    "i4_paged_gqa_chunk": (_i, [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz,
-                                _vp]),
+    "i4_paged_gqa_chunk": (_i, [_vp, _vp]),
     "i4_kv_pages_ws_bytes": (_sz, [_i, _i]),
     "i4_kv_pages_copy": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp]),
     "i4_kv_pages_reserve": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
@@ -324,6 +336,13 @@ def silu_mul(gate_up, out=None, stream=None):
 
 # ------------------------------------------------------------------ several new tokens of several sequences
 
+# The argument structures of the header (RopeChunkArgs, ChunkAttnArgs, KvCacheDesc) as the calls below build them: packing
+# takes a quarter of a ctypes structure's time, and one pointer less of ctypes' conversion than twenty arguments.
+_ROPE_CHUNK = struct.Struct("@Qq7Q11i0q")
+_CHUNK_ATTN = struct.Struct("@Qq8Q10if0q")
+_CACHE = struct.Struct("@3Q4i0q")
+
+
 def _refuse(name: str, what: str):
     raise I4Error(I4_EINVAL, f"{name}: {what}")
 
@@ -416,10 +435,11 @@ def rope_append_chunk(qkv, q_start, ctx_len, cs, Hq: int, Hkv: int, k_pool, v_po
                       f"q_out {tuple(q_out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
     if T == 0 or B == 0:
         return q_out
-    _check(lib().i4_rope_append_chunk(qkv.data_ptr(), qkv.stride(0) if T > 1 else width, q_start.data_ptr(), ctx_len.data_ptr(),
-                                      cs.data_ptr(), max_pos, half * 2, int(interleaved), T, B, Hq, Hkv, D,
-                                      q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), P,
-                                      max_pages, num_pages, _raw_stream(stream, dev)), name)
+    _check(lib().i4_rope_append_chunk(
+        _ROPE_CHUNK.pack(qkv.data_ptr(), qkv.stride(0) if T > 1 else width, q_start.data_ptr(), ctx_len.data_ptr(),
+                         cs.data_ptr(), q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(),
+                         max_pos, half * 2, 1 if interleaved else 0, T, B, Hq, Hkv, D, P, max_pages, num_pages),
+        _raw_stream(stream, dev)), name)
     return q_out
 
 
@@ -452,11 +472,12 @@ def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, w
                       f"{tuple(out.shape)}, {B} page-table rows, q_start {q_start.numel()}")
     if T == 0 or B == 0:
         return out
-    _check(lib().i4_paged_gqa_chunk(q.data_ptr(), q.stride(0) if T > 1 else Hq * D, k_pool.data_ptr(), v_pool.data_ptr(),
-                                    page_table.data_ptr(), q_start.data_ptr(), ctx_len.data_ptr(), out.data_ptr(), T, B, Hq,
-                                    Hkv, D, P, max_pages, num_pages, int(window), int(max_q),
-                                    D ** -0.5 if scale is None else float(scale), ws.data_ptr(), ws.numel(),
-                                    _raw_stream(stream, dev)), name)
+    _check(lib().i4_paged_gqa_chunk(
+        _CHUNK_ATTN.pack(q.data_ptr(), q.stride(0) if T > 1 else Hq * D, k_pool.data_ptr(), v_pool.data_ptr(),
+                         page_table.data_ptr(), q_start.data_ptr(), ctx_len.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                         ws.numel(), T, B, Hq, Hkv, D, P, max_pages, num_pages, window, max_q,
+                         D ** -0.5 if scale is None else scale),
+        _raw_stream(stream, dev)), name)
     return out
 
 
@@ -489,7 +510,6 @@ def _cache_desc(name: str, page_table, ctx_len, refs, page_size: int, ws, *lists
 
 
 _CACHE_DIMS = (2, 1, 1, 1, 1, 1, 1)  # page_table, then lists and the workspace
-_CACHE = struct.Struct("@3Q4i")  # i4_kv_cache (KvCacheDesc), packed in a quarter of a ctypes structure's time
 
 
 def kv_pages_ws_bytes(num_pages: int, n_seqs: int) -> int:

@@ -1010,10 +1010,10 @@ using namespace i4;
 
 extern "C" size_t i4_paged_gqa_chunk_ws_bytes(void) { return kWsBytes; }
 
-extern "C" int i4_paged_gqa_chunk(const uint16_t *q, long long q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
-                                  const int32_t *page_table, const int32_t *q_start, const int32_t *ctx_len, uint16_t *out, int T,
-                                  int B, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages, int window,
-                                  int max_q, float scale, void *ws, size_t ws_bytes, void *stream) {
+extern "C" int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream) {
+    if (!args) return fail(I4_EINVAL, "i4_paged_gqa_chunk: null args");
+    const auto [q, q_stride, k_pool, v_pool, page_table, q_start, ctx_len, out, ws, ws_bytes, T, B, Hq, Hkv, D, page_size,
+                max_pages_per_seq, num_pages, window, max_q, scale] = *args;
     if (!q || !k_pool || !v_pool || !page_table || !q_start || !ctx_len || !out)
         return fail(I4_EINVAL, "i4_paged_gqa_chunk: null pointer");
     if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || max_pages_per_seq < 1 || num_pages < 1 || window < 0 || max_q < 0)

@@ -174,11 +174,10 @@ extern "C" int i4_rope_table(float *cs, int max_pos, int rotary_dim, double thet
     return launch_check("i4_rope_table");
 }
 
-extern "C" int i4_rope_append_chunk(const uint16_t *qkv, long long qkv_stride, const int32_t *q_start,
-                                    const int32_t *ctx_len, const float *cs, int max_pos, int rotary_dim,
-                                    int interleaved, int T, int B, int Hq, int Hkv, int D, uint16_t *q_out,
-                                    uint16_t *k_pool, uint16_t *v_pool, const int32_t *page_table, int page_size,
-                                    int max_pages_per_seq, int num_pages, void *stream) {
+extern "C" int i4_rope_append_chunk(const i4_rope_chunk_args *args, void *stream) {
+    if (!args) return fail(I4_EINVAL, "i4_rope_append_chunk: null args");
+    const auto [qkv, qkv_stride, q_start, ctx_len, cs, q_out, k_pool, v_pool, page_table, max_pos, rotary_dim, interleaved, T, B, Hq, Hkv, D,
+                page_size, max_pages_per_seq, num_pages] = *args;
     if (!qkv || !q_start || !ctx_len || !cs || !q_out || !k_pool || !v_pool || !page_table)
         return fail(I4_EINVAL, "i4_rope_append_chunk: null pointer");
     if (D != 128) return fail(I4_EUNSUPPORTED, "i4_rope_append_chunk: head_dim %d (only 128)", D);

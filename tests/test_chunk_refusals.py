@@ -6,16 +6,22 @@ import pytest
 FAKE = 1 << 20  # an address that is never followed: validation fails first
 
 
-def status(fn, base, **change):
+FIELDS = dict(k="k_pool", v="v_pool", table="page_table", ctx="ctx_len", page="page_size", max_pages="max_pages_per_seq",
+              pages="num_pages", stride="qkv_stride", rd="rotary_dim", inter="interleaved")
+
+
+def status(fn, base, args=None, **change):
     names = [n for n, _ in base]
-    args = dict(base, **change)
+    values = dict(base, **change)
     assert set(change) <= set(names)
-    return fn(*[args[n] for n in names])
+    if args is None:
+        return fn(*[values[n] for n in names])
+    return fn(ctypes.byref(args(**{FIELDS.get(n, n): v for n, v in values.items()})), None)
 
 
 ATTN = [("q", FAKE), ("q_stride", 28 * 128), ("k", FAKE), ("v", FAKE), ("table", FAKE), ("q_start", FAKE), ("ctx", FAKE), ("out", FAKE),
         ("T", 10), ("B", 2), ("Hq", 28), ("Hkv", 4), ("D", 128), ("page", 16), ("max_pages", 8), ("pages", 20), ("window", 0),
-        ("max_q", 0), ("scale", 0.1), ("ws", FAKE), ("ws_bytes", 1), ("stream", None)]
+        ("max_q", 0), ("scale", 0.1), ("ws", FAKE), ("ws_bytes", 1)]
 
 
 @pytest.mark.parametrize("change,want", [
@@ -30,13 +36,13 @@ ATTN = [("q", FAKE), ("q_stride", 28 * 128), ("k", FAKE), ("v", FAKE), ("table",
     (dict(ws=None), -1), (dict(), -1), (dict(ws_bytes=1 << 40, ws=FAKE + 16), -2),
 ])
 def test_attention(i4lib, change, want):
-    assert status(i4lib.lib().i4_paged_gqa_chunk, ATTN, **change) == want
+    assert status(i4lib.lib().i4_paged_gqa_chunk, ATTN, i4lib.ChunkAttnArgs, **change) == want
     assert i4lib.lib().i4_last_error()
 
 
 ROPE = [("qkv", FAKE), ("stride", 36 * 128), ("q_start", FAKE), ("ctx", FAKE), ("cs", FAKE), ("max_pos", 100), ("rd", 128), ("inter", 0),
         ("T", 4), ("B", 2), ("Hq", 28), ("Hkv", 4), ("D", 128), ("q_out", FAKE), ("k", FAKE), ("v", FAKE), ("table", FAKE), ("page", 16),
-        ("max_pages", 4), ("pages", 8), ("stream", None)]
+        ("max_pages", 4), ("pages", 8)]
 
 
 @pytest.mark.parametrize("change,want", [
@@ -47,7 +53,22 @@ ROPE = [("qkv", FAKE), ("stride", 36 * 128), ("q_start", FAKE), ("ctx", FAKE), (
     (dict(qkv=FAKE + 8), -2), (dict(cs=FAKE + 8), -2), (dict(q_out=FAKE + 8), -2), (dict(k=FAKE + 8), -2), (dict(ctx=FAKE + 2), -2),
 ])
 def test_rope_append(i4lib, change, want):
-    assert status(i4lib.lib().i4_rope_append_chunk, ROPE, **change) == want
+    assert status(i4lib.lib().i4_rope_append_chunk, ROPE, i4lib.RopeChunkArgs, **change) == want
+
+
+def test_null_arguments(i4lib):
+    assert i4lib.lib().i4_rope_append_chunk(None, None) == -1
+    assert i4lib.lib().i4_paged_gqa_chunk(None, None) == -1
+
+
+def test_packed_arguments_are_the_structures(i4lib):
+    """The calls pack the header's structures themselves: the same sizes, and every field at its place."""
+    for packed, st in ((i4lib._ROPE_CHUNK, i4lib.RopeChunkArgs), (i4lib._CHUNK_ATTN, i4lib.ChunkAttnArgs),
+                       (i4lib._CACHE, i4lib.KvCacheDesc)):
+        names = [n for n, _ in st._fields_]
+        assert packed.size == ctypes.sizeof(st)
+        got = st.from_buffer_copy(packed.pack(*range(1, len(names) + 1)))
+        assert [getattr(got, n) for n in names] == list(range(1, len(names) + 1))
 
 
 TABLE = [("cs", FAKE), ("max_pos", 10), ("rd", 128), ("theta", 1e6), ("scaling", 2), ("factor", 4.0), ("original", 1024), ("stream", None)]
