@@ -29,7 +29,7 @@
 //    254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.)
 //
 // Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows costs
-// 3072 cycles of 3300 measured, and under a steady load the GPU's power limit holds the clock near 1.6 GHz. 512 tokens behind 32768 positions
+// 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the clock near 1.6 GHz. 512 tokens behind 32768 positions
 // (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt
 // of 8192: 425 and 494 us. Few rows are bound by the chain of dependent steps: four single tokens at up to 2049 positions take 16 us,
 // 3.5 to the first tile (lengths, scans, first loads), 2 a tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.

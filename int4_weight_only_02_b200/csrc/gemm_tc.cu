@@ -399,6 +399,9 @@ int launch_int4_gemm(const uint32_t *w, const uint16_t *s, const uint16_t *x, co
     }
 }
 
+int read_chunk_error(int reset);  // attention_chunk.cu
+
+// The error flags of the tcgen05 kernels: this file's and the chunk attention's.
 int read_gemm_error(int reset) {
     int v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof v);
@@ -408,7 +411,8 @@ int read_gemm_error(int reset) {
         e = cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof zero);
         if (e != cudaSuccess) return cuda_check(e, "clearing the GEMM error flag");
     }
-    return v;
+    const int chunk = read_chunk_error(reset);
+    return chunk < 0 || !v ? chunk : v;
 }
 
 }  // namespace i4

@@ -1070,7 +1070,6 @@ int read_gemv_error(int reset) {
 int read_attn_error(int reset);
 int read_persist_error(int reset);
 int read_gemm_error(int reset);
-int read_chunk_error(int reset);
 
 }  // namespace i4
 
@@ -1080,11 +1079,9 @@ extern "C" int i4_device_error(int reset) {
     const int b = i4::read_attn_error(reset);
     const int c = i4::read_persist_error(reset);
     const int d = i4::read_gemm_error(reset);
-    const int e = i4::read_chunk_error(reset);
     if (a < 0) return a;
     if (b < 0) return b;
     if (c < 0) return c;
     if (d < 0) return d;
-    if (e < 0) return e;
-    return a ? a : (b ? b : (c ? c : (d ? d : e)));
+    return a ? a : (b ? b : (c ? c : d));
 }
