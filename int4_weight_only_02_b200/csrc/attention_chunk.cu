@@ -28,11 +28,12 @@
 //    NQ = 1, for chunks that fit one slot, two CTAs share an SM. (Whole tiles of 128 with the slots taking turns come out the same,
 //    254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.)
 //
-// Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows costs
-// 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the clock near 1.6 GHz. 512 tokens behind 32768 positions
-// (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt
-// of 8192: 425 and 494 us. Few rows are bound by the chain of dependent steps: four single tokens at up to 2049 positions take 16 us,
-// 3.5 to the first tile (lengths, scans, first loads), 2 a tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.
+// Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows
+// costs 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the
+// clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a
+// steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 425 and 494 us. Few rows are bound by the chain of dependent
+// steps: four single tokens at up to 2049 positions take 16 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
+// tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.
 #include <cmath>
 
 #include "chunk.cuh"
@@ -71,7 +72,8 @@ __device__ int g_chunk_error = 0;
 
 // Where a unit is cut at the beginning of a CTA's stretch: what the joining kernel needs.
 struct Cut {
-    int valid, last, tokens, row, g;  // parts: CTA c-1's last, then the first of c .. last; the unit's tokens begin at this row of q
+    // parts: CTA c - 1's last, then the first of c .. last; the unit's tokens begin at this row of q
+    int valid, last, tokens, row, g;
 };
 
 struct ChunkAttnParams {
@@ -218,7 +220,8 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
     using C = Cfg<NQ>;
     constexpr int NT = C::kThreads, V = C::kUnitCost;
     const int tid = threadIdx.x, size = NQ * p.slot_tokens;
-    int *sums = scratch, *first = scratch + 32, *tokens = first + NT, *pos = tokens + NT;  // units before sequence b0 + j; the sequence
+    // first: units before sequence b0 + j; tokens, pos: its new tokens and the first one's position
+    int *sums = scratch, *first = scratch + 32, *tokens = first + NT, *pos = tokens + NT;
     if (tid == 0) {
         *out = {0, 0, 0, 0, 0, 0, 0, 0};
         p.cuts[blockIdx.x].valid = 0;
@@ -410,12 +413,13 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
 
 template <int NQ>
 __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
-    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ ChunkAttnParams p) {
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkAttnParams p) {
     using C = Cfg<NQ>;
     constexpr int S = C::kStages, kMmaWarp = NQ * 4, kLoadWarp = kMmaWarp + NQ;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], q_free[NQ], s_full[NQ][2], p_full[NQ][2], pv_done[NQ][2], o_free[NQ], all_done;
+    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], q_full[NQ], q_free[NQ], s_full[NQ][2], p_full[NQ][2];
+    __shared__ __align__(8) uint64_t pv_done[NQ][2], o_free[NQ], all_done;
     __shared__ uint32_t tmem_base;
     __shared__ Stretch stretch;
     __shared__ int stop_flag;
@@ -454,6 +458,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     if (warp == kLoadWarp && lane < 3)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &tm_q : (lane == 1 ? &tm_k : &tm_v)) : "memory");
     find_stretch<NQ>(p, &stretch, reinterpret_cast<int *>(gbase));
+    fence_async_smem();  // its scratch lies where the first copy of Q will
     grid_dep_launch();  // the joining kernel may come up; it waits for this grid's end before it reads anything
     fence_before_sync();
     __syncthreads();
@@ -465,162 +470,163 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     if (stretch.left <= 0) {
         // no work: straight to the end
     } else if (warp >= kMmaWarp) {
-    // The rows of Q of one slot's piece: tokens behind the sequence's are another's, or zeros behind the last row; nothing
-    // that comes of them is stored.
-    auto load_q = [&](const Piece &c, int s) {
-        if (lane == 0) {
-            mbar_expect_tx(&q_full[s], (unsigned)(p.slot_tokens * G) * 256u);
+        // The rows of Q of one slot's piece: tokens behind the sequence's are another's, or zeros behind the last row; nothing
+        // that comes of them is stored.
+        auto load_q = [&](const Piece &c, int s) {
+            if (lane == 0) {
+                mbar_expect_tx(&q_full[s], (unsigned)(p.slot_tokens * G) * 256u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                tma_load_4d(base + s * kTileBytes + h * kHalf, &tm_q, 64 * h, c.g * G, c.row0 + c.tok0 + s * p.slot_tokens, 0, &q_full[s]);
-        }
-    };
-    if (warp > kLoadWarp) {
-        // ---------------- rows of Q (NQ = 2; with NQ = 1 the load warp's own)
-        unsigned uses[NQ] = {};
-        bool ok = true;
-        while (ok && walk.next(pc)) {
-#pragma unroll
-            for (int s = 0; s < NQ; ++s) {
-                const int3 r = slot_tiles(p, pc, s);
-                if (r.y <= r.x) continue;
-                if (ok && uses[s] > 0) ok = wait_or_stop(&q_free[s], (uses[s] - 1) & 1, stop);
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) load_q(pc, s);
-                uses[s] += ok;
+                for (int h = 0; h < 2; ++h)
+                    tma_load_4d(base + s * kTileBytes + h * kHalf, &tm_q, 64 * h, c.g * G, c.row0 + c.tok0 + s * p.slot_tokens, 0,
+                                &q_full[s]);
             }
-        }
-        if (!ok && lane == 0)  // let the copies in flight land
-            for (int s = 0; s < NQ; ++s)
-                if (uses[s] > 0) mbar_wait(&q_full[s], (uses[s] - 1) & 1);
-        __syncwarp();
-    } else if (warp == kLoadWarp) {
-        // ---------------- K and V tiles: K0 V0 K1 V1 ...
-        const int np = kTile / p.page_size;  // pages of a tile
-        const int half = lane / np, pg = lane % np;
-        const bool loads = lane < 2 * np;
-        unsigned it = 0, uses = 0;
-        bool ok = true;
-        while (ok && walk.next(pc)) {
-            for (int t = pc.t0; ok && t < pc.t1; ++t) {
-                const int idx = t * np + pg;
-                int page = p.num_pages;  // out of range: the copy fills zeros
-                if (loads && idx * p.page_size < pc.see.y && (idx + 1) * p.page_size > pc.see.x) {
-                    const int e = p.page_table[(size_t)pc.b * p.max_pages + idx];
-                    if (e >= 0 && e < p.num_pages) page = e;
+        };
+        if (warp > kLoadWarp) {
+            // ---------------- rows of Q (NQ = 2; with NQ = 1 the load warp's own)
+            unsigned uses[NQ] = {};
+            bool ok = true;
+            while (ok && walk.next(pc)) {
+#pragma unroll
+                for (int s = 0; s < NQ; ++s) {
+                    const int3 r = slot_tiles(p, pc, s);
+                    if (r.y <= r.x) continue;
+                    if (ok && uses[s] > 0) ok = wait_or_stop(&q_free[s], (uses[s] - 1) & 1, stop);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok) load_q(pc, s);
+                    uses[s] += ok;
                 }
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const unsigned st = it % S, use = it / S;
-                    ok = use == 0 || wait_or_stop(&kv_empty[st], (use - 1) & 1, stop);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
+            }
+            if (!ok && lane == 0)  // let the copies in flight land
+                for (int s = 0; s < NQ; ++s)
+                    if (uses[s] > 0) mbar_wait(&q_full[s], (uses[s] - 1) & 1);
+            __syncwarp();
+        } else if (warp == kLoadWarp) {
+            // ---------------- K and V tiles: K0 V0 K1 V1 ...
+            const int np = kTile / p.page_size;  // pages of a tile
+            const int half = lane / np, pg = lane % np;
+            const bool loads = lane < 2 * np;
+            unsigned it = 0, uses = 0;
+            bool ok = true;
+            while (ok && walk.next(pc)) {
+                for (int t = pc.t0; ok && t < pc.t1; ++t) {
+                    const int idx = t * np + pg;
+                    int page = p.num_pages;  // out of range: the copy fills zeros
+                    if (loads && idx * p.page_size < pc.see.y && (idx + 1) * p.page_size > pc.see.x) {
+                        const int e = p.page_table[(size_t)pc.b * p.max_pages + idx];
+                        if (e >= 0 && e < p.num_pages) page = e;
                     }
-                    if (lane == 0) mbar_expect_tx(&kv_full[st], kTileBytes);
-                    __syncwarp();
-                    if (loads)
-                        tma_load_4d(ring + st * kTileBytes + half * kHalf + pg * p.page_size * 128, kv ? &tm_v : &tm_k, half * 64, 0,
-                                    pc.g, page, &kv_full[st]);
-                    if (NQ == 1 && t == pc.t0 && kv == 0) {  // behind the piece's first K tile
-                        if (uses > 0) ok = wait_or_stop(&q_free[0], (uses - 1) & 1, stop);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) {
-                            ++it;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const unsigned st = it % S, use = it / S;
+                        ok = use == 0 || wait_or_stop(&kv_empty[st], (use - 1) & 1, stop);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
                             break;
                         }
-                        load_q(pc, 0);
+                        if (lane == 0) mbar_expect_tx(&kv_full[st], kTileBytes);
+                        __syncwarp();
+                        if (loads)
+                            tma_load_4d(ring + st * kTileBytes + half * kHalf + pg * p.page_size * 128, kv ? &tm_v : &tm_k,
+                                        half * 64, 0, pc.g, page, &kv_full[st]);
+                        if (NQ == 1 && t == pc.t0 && kv == 0) {  // behind the piece's first K tile
+                            if (uses > 0) ok = wait_or_stop(&q_free[0], (uses - 1) & 1, stop);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) {
+                                ++it;
+                                break;
+                            }
+                            load_q(pc, 0);
+                            ++uses;
+                        }
+                    }
+                }
+            }
+            if (!ok && lane == 0) {  // let the copies in flight land before the CTA's memory goes
+                for (unsigned k = it > S ? it - S : 0; k < it; ++k) mbar_wait(&kv_full[k % S], (k / S) & 1);
+                if (NQ == 1 && uses > 0) mbar_wait(&q_full[0], (uses - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp < kMmaWarp + NQ) {
+            // ---------------- S = Q K^T and O += P V of slot s. One warp per slot: both slots' products issued by one warp took
+            // longer than the tensor cores' own work
+            constexpr uint32_t idesc_qk = idesc_f16(kRows, kStep), idesc_pv = idesc_f16(kRows, 128) | kIdescBMajorMN;
+            const int s = (int)uniform((uint32_t)(warp - kMmaWarp));
+            const uint32_t tS = tmem + 128 * s, tO = tmem + 128 * (NQ + s);
+            const uint64_t qd = desc_sw128(base + s * kTileBytes), kd0 = desc_sw128(ring), vd0 = desc_sw128_mn(ring, kHalf);
+            unsigned it = 0, uses = 0, steps = 0;  // ring entries, pieces and tiles so far
+            bool ok = true;
+            while (ok && walk.next(pc)) {
+                const int3 r = slot_tiles(p, pc, s);
+                if (pc.t1 <= pc.t0) continue;
+#pragma unroll 1
+                for (int j = pc.t0 - 1; j < pc.t1; ++j, it += 2) {
+                    // entries it - 1: V of tile j, it: K of tile j + 1
+                    const unsigned sv = (it - 1) % S, sk = it % S;
+                    const bool has_v = j >= pc.t0, has_k = j + 1 < pc.t1;
+                    const bool pv = j >= r.x && j < r.y, qk = j + 1 >= r.x && j + 1 < r.y;
+                    if (has_v) {
+                        ok = wait_or_stop(&kv_full[sv], ((it - 1) / S) & 1, stop);
+                        const int t = j * kTile;
+                        if (ok && (t < pc.see.x || t + kTile > pc.see.y)) {
+                            // rows of V that the unit does not see may hold anything, NaN included: zero them (both slots' warps
+                            // write the same zeros)
+                            for (int e = lane; e < 2 * kTile * 8; e += 32) {
+                                const int u = (e >> 3) & (kTile - 1);
+                                if (t + u < pc.see.x || t + u >= pc.see.y)
+                                    *reinterpret_cast<uint4 *>(gbase + (NQ + sv) * kTileBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async_smem();
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && has_k) ok = wait_or_stop(&kv_full[sk], (it / S) & 1, stop);
+                    if (ok && qk && j + 1 == r.x) ok = wait_or_stop(&q_full[s], uses & 1, stop);
+                    if (ok && pv && j == r.x) {
+                        if (uses > 0) ok = wait_or_stop(&o_free[s], (uses - 1) & 1, stop);
                         ++uses;
                     }
-                }
-            }
-        }
-        if (!ok && lane == 0) {  // let the copies in flight land before the CTA's memory goes
-            for (unsigned k = it > S ? it - S : 0; k < it; ++k) mbar_wait(&kv_full[k % S], (k / S) & 1);
-            if (NQ == 1 && uses > 0) mbar_wait(&q_full[0], (uses - 1) & 1);
-        }
-        __syncwarp();
-    } else if (warp < kMmaWarp + NQ) {
-        // ---------------- S = Q K^T and O += P V of slot s. One warp per slot: a tile takes a warp some 150 instructions that
-        // nothing else on its scheduler shares, and both slots' in one warp took longer than the tensor cores' own work
-        constexpr uint32_t idesc_qk = idesc_f16(kRows, kStep), idesc_pv = idesc_f16(kRows, 128) | kIdescBMajorMN;
-        const int s = (int)uniform((uint32_t)(warp - kMmaWarp));
-        const uint32_t tS = tmem + 128 * s, tO = tmem + 128 * (NQ + s);
-        const uint64_t qd = desc_sw128(base + s * kTileBytes), kd0 = desc_sw128(ring), vd0 = desc_sw128_mn(ring, kHalf);
-        unsigned it = 0, uses = 0, steps = 0;  // ring entries, pieces and tiles so far
-        bool ok = true;
-        while (ok && walk.next(pc)) {
-            const int3 r = slot_tiles(p, pc, s);
-            if (pc.t1 <= pc.t0) continue;
+                    const uint64_t vd = vd0 + uniform(sv) * (kTileBytes >> 4), kd = kd0 + uniform(sk) * (kTileBytes >> 4);
+                    const int more = j > r.x;
 #pragma unroll 1
-            for (int j = pc.t0 - 1; j < pc.t1; ++j, it += 2) {
-                // entries it - 1: V of tile j, it: K of tile j + 1
-                const unsigned sv = (it - 1) % S, sk = it % S;
-                const bool has_v = j >= pc.t0, has_k = j + 1 < pc.t1;
-                const bool pv = j >= r.x && j < r.y, qk = j + 1 >= r.x && j + 1 < r.y;
-                if (has_v) {
-                    ok = wait_or_stop(&kv_full[sv], ((it - 1) / S) & 1, stop);
-                    const int t = j * kTile;
-                    if (ok && (t < pc.see.x || t + kTile > pc.see.y)) {
-                        // rows of V that the unit does not see may hold anything, NaN included: zero them (both slots' warps
-                        // write the same zeros)
-                        for (int e = lane; e < 2 * kTile * 8; e += 32) {
-                            const int u = (e >> 3) & (kTile - 1);
-                            if (t + u < pc.see.x || t + u >= pc.see.y)
-                                *reinterpret_cast<uint4 *>(gbase + (NQ + sv) * kTileBytes + e * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_smem();
-                    }
-                    __syncwarp();
-                }
-                if (ok && has_k) ok = wait_or_stop(&kv_full[sk], (it / S) & 1, stop);
-                if (ok && qk && j + 1 == r.x) ok = wait_or_stop(&q_full[s], uses & 1, stop);
-                if (ok && pv && j == r.x) {
-                    if (uses > 0) ok = wait_or_stop(&o_free[s], (uses - 1) & 1, stop);
-                    ++uses;
-                }
-                const uint64_t vd = vd0 + uniform(sv) * (kTileBytes >> 4), kd = kd0 + uniform(sk) * (kTileBytes >> 4);
-                const int more = j > r.x;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {  // the halves of the tile: P V of one, then the next tile's S over it
-                    if (ok && pv) ok = wait_or_stop(&p_full[s][h], steps & 1, stop);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    fence_after_sync();
-                    if (elect_one()) {
-                        if (pv) {
+                    for (int h = 0; h < 2; ++h) {  // the halves of the tile: P V of one, then the next tile's S over it
+                        if (ok && pv) ok = wait_or_stop(&p_full[s][h], steps & 1, stop);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        fence_after_sync();
+                        if (elect_one()) {
+                            if (pv) {
 #pragma unroll
-                            for (int kk = 0; kk < kStep / 16; ++kk)
-                                umma_f16_ta(tO, tS + kStep * h + 8 * kk, vd + (h * (kStep / 16) + kk) * (2048 >> 4), idesc_pv,
-                                            kk > 0 ? 1 : (more | h));
-                            umma_commit(&pv_done[s][h]);
-                        }
-                        if (qk) {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                                umma_f16(tS + kStep * h, qd + o, kd + o + h * (kStep * 128 >> 4), idesc_qk, kk > 0 ? 1 : 0);
+                                for (int kk = 0; kk < kStep / 16; ++kk)
+                                    umma_f16_ta(tO, tS + kStep * h + 8 * kk, vd + (h * (kStep / 16) + kk) * (2048 >> 4), idesc_pv,
+                                                kk > 0 ? 1 : (more | h));
+                                umma_commit(&pv_done[s][h]);
                             }
-                            umma_commit(&s_full[s][h]);
+                            if (qk) {
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk) {
+                                    const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                                    umma_f16(tS + kStep * h, qd + o, kd + o + h * (kStep * 128 >> 4), idesc_qk, kk > 0 ? 1 : 0);
+                                }
+                                umma_commit(&s_full[s][h]);
+                            }
+                            if (h == 1) {
+                                if (has_v) umma_commit(&kv_empty[sv]);
+                                if (has_k) umma_commit(&kv_empty[sk]);
+                                if (qk && j + 2 == r.y) umma_commit(&q_free[s]);
+                            }
                         }
-                        if (h == 1) {
-                            if (has_v) umma_commit(&kv_empty[sv]);
-                            if (has_k) umma_commit(&kv_empty[sk]);
-                            if (qk && j + 2 == r.y) umma_commit(&q_free[s]);
-                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    steps += pv;
+                    if (!__all_sync(0xffffffffu, ok)) break;
                 }
-                steps += pv;
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok = __all_sync(0xffffffffu, ok);
+                it -= 2;
             }
-            ok = __all_sync(0xffffffffu, ok);
-            it -= 2;
+            // nothing of this slot is in flight on the tensor cores when the CTA leaves
+            if (elect_one()) umma_commit(&all_done);
+            if (!mbar_wait(&all_done, 0)) record_error(&g_chunk_error, 1);
+            __syncwarp();
         }
-        // nothing of this slot is in flight on the tensor cores when the CTA leaves
-        if (elect_one()) umma_commit(&all_done);
-        if (!mbar_wait(&all_done, 0)) record_error(&g_chunk_error, 1);
-        __syncwarp();
-    }
     } else {
         // ---------------- softmax of slot s: thread = row
         const int s = warp >> 2, wq = warp & 3, row = tid & 127;
@@ -709,7 +715,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                         uint4 v[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            v[k] = make_uint4(o[16 * i + 4 * k], o[16 * i + 4 * k + 1], o[16 * i + 4 * k + 2], o[16 * i + 4 * k + 3]);
+                            v[k] = make_uint4(o[16 * i + 4 * k], o[16 * i + 4 * k + 1], o[16 * i + 4 * k + 2],
+                                              o[16 * i + 4 * k + 3]);
                         transpose4(v);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -723,7 +730,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 if (lane == 0) mbar_arrive(&o_free[s]);
             }
             // rows that met a NaN or an infinity, and whose own scores are fine, are summed again over what they see
-            unsigned again = __ballot_sync(0xffffffffu, mine && any && !(bad[0] + bad[1] + (bad[2] + bad[3]) == 0.f) && fabsf(l) < INFINITY);
+            const bool fine = bad[0] + bad[1] + (bad[2] + bad[3]) == 0.f;
+            unsigned again = __ballot_sync(0xffffffffu, mine && any && !fine && fabsf(l) < INFINITY);
             while (again) {
                 const int k = __ffs(again) - 1;
                 again &= again - 1;
@@ -735,7 +743,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                 const int tk = __shfl_sync(0xffffffffu, tok, k), hk = __shfl_sync(0xffffffffu, head, k);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (mk > -INFINITY)
-                    v = plain_row(p, last.b, last.g, p.q + (size_t)(last.row0 + tk) * p.q_stride + (size_t)hk * 128, lo, hi, qs, mk * qs);
+                    v = plain_row(p, last.b, last.g, p.q + (size_t)(last.row0 + tk) * p.q_stride + (size_t)hk * 128, lo, hi, qs,
+                                  mk * qs);
                 if (last.whole) {
                     uint16_t *d = p.out + ((size_t)(last.row0 + tk) * p.Hq + hk) * 128 + 4 * lane;
                     d[0] = float_to_half_bits(v.x * inv);
@@ -812,7 +821,8 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 v = ffma2(make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), qs2, mm2);
+                        const float2 sc = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
+                        float2 v = ffma2(sc, qs2, mm2);
                         v = make_float2(ex2(v.x), ex2(v.y));
                         if (i & 1)
                             sum1 = fadd2(sum1, v);
@@ -854,77 +864,79 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
     constexpr int U = 8 / R;  // parts of each of a warp's R rows that are in flight together
 #pragma unroll 1
     for (int row0 = blockIdx.y * 32 + R * (threadIdx.x >> 5); row0 < (int)blockIdx.y * 32 + 32; row0 += 8 * R) {
-    bool in[R];
-    float M[R], L[R];
-    float4 o[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int in_slot = (row0 + i) % kRows / G;
-        in[i] = in_slot < p.slot_tokens && (row0 + i) / kRows * p.slot_tokens + in_slot < c.tokens;
-        M[i] = -INFINITY;
-        L[i] = 0.f;
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (!in[0]) return;  // rows of a slot without tokens are its last
-    float2 ml[R];  // of part `lane`; the parts behind 32 are read again below
-    auto load_ml = [&](int k0) {
+        bool in[R];
+        float M[R], L[R];
+        float4 o[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
-            if (in[i] && k0 + lane < parts) ml[i] = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row0 + i];
+            const int in_slot = (row0 + i) % kRows / G;
+            in[i] = in_slot < p.slot_tokens && (row0 + i) / kRows * p.slot_tokens + in_slot < c.tokens;
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    };
-    for (int k0 = (parts - 1) & ~31; k0 >= 0; k0 -= 32) {
-        load_ml(k0);
+        if (!in[0]) return;  // rows of a slot without tokens are its last
+        float2 ml[R];  // of part `lane`; the parts behind 32 are read again below
+        auto load_ml = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) M[i] = fmaxf(M[i], ml[i].x);
-    }
+            for (int i = 0; i < R; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                if (in[i] && k0 + lane < parts) ml[i] = p.part_ml[(size_t)slot(k0 + lane) * unit_rows + row0 + i];
+            }
+        };
+        for (int k0 = (parts - 1) & ~31; k0 >= 0; k0 -= 32) {
+            load_ml(k0);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-        if (k0 > 0) load_ml(k0);
-        float w[R];
-        unsigned there[R];  // parts that saw something: the others have no O
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            w[i] = ml[i].x > -INFINITY ? exp2f(ml[i].x - M[i]) : 0.f;
-            L[i] += warp_sum(w[i] * ml[i].y);
-            there[i] = __ballot_sync(0xffffffffu, ml[i].x > -INFINITY);
+            for (int i = 0; i < R; ++i) M[i] = fmaxf(M[i], ml[i].x);
         }
-        const int n = min(32, parts - k0);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], x));
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            if (k0 > 0) load_ml(k0);
+            float w[R];
+            unsigned there[R];  // parts that saw something: the others have no O
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                w[i] = ml[i].x > -INFINITY ? exp2f(ml[i].x - M[i]) : 0.f;
+                L[i] += warp_sum(w[i] * ml[i].y);
+                there[i] = __ballot_sync(0xffffffffu, ml[i].x > -INFINITY);
+            }
+            const int n = min(32, parts - k0);
 #pragma unroll 1
-        for (int k1 = 0; k1 < n; k1 += U) {
-            float4 v[U][R];
+            for (int k1 = 0; k1 < n; k1 += U) {
+                float4 v[U][R];
 #pragma unroll
-            for (int k = 0; k < U; ++k)
+                for (int k = 0; k < U; ++k)
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if ((there[i] >> (k1 + k)) & 1)
-                        v[k][i] = reinterpret_cast<const float4 *>(p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row0 + i) * 32 + lane];
-                }
+                    for (int i = 0; i < R; ++i) {
+                        v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if ((there[i] >> (k1 + k)) & 1)
+                            v[k][i] = reinterpret_cast<const float4 *>(
+                                p.part_o)[((size_t)slot(k0 + k1 + k) * unit_rows + row0 + i) * 32 + lane];
+                    }
 #pragma unroll
-            for (int k = 0; k < U; ++k)
+                for (int k = 0; k < U; ++k)
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float wk = __shfl_sync(0xffffffffu, w[i], k1 + k);
-                    o[i] = make_float4(fmaf(wk, v[k][i].x, o[i].x), fmaf(wk, v[k][i].y, o[i].y), fmaf(wk, v[k][i].z, o[i].z),
-                                       fmaf(wk, v[k][i].w, o[i].w));
-                }
+                    for (int i = 0; i < R; ++i) {
+                        const float wk = __shfl_sync(0xffffffffu, w[i], k1 + k);
+                        o[i] = make_float4(fmaf(wk, v[k][i].x, o[i].x), fmaf(wk, v[k][i].y, o[i].y), fmaf(wk, v[k][i].z, o[i].z),
+                                           fmaf(wk, v[k][i].w, o[i].w));
+                    }
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        if (!in[i]) continue;
-        const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
-        const int row = row0 + i, in_slot = row % kRows / G, tok = row / kRows * p.slot_tokens + in_slot;
-        uint2 h;
-        h.x = h2_bits(__floats2half2_rn(o[i].x * inv, o[i].y * inv));
-        h.y = h2_bits(__floats2half2_rn(o[i].z * inv, o[i].w * inv));
-        *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + c.g * G + row % kRows - in_slot * G) * 128 + 4 * lane) = h;
-    }
+        for (int i = 0; i < R; ++i) {
+            if (!in[i]) continue;
+            const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+            const int row = row0 + i, in_slot = row % kRows / G, tok = row / kRows * p.slot_tokens + in_slot;
+            uint2 h;
+            h.x = h2_bits(__floats2half2_rn(o[i].x * inv, o[i].y * inv));
+            h.y = h2_bits(__floats2half2_rn(o[i].z * inv, o[i].w * inv));
+            const int hq = c.g * G + row % kRows - in_slot * G;
+            *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + hq) * 128 + 4 * lane) = h;
+        }
     }
 }
 
@@ -972,7 +984,8 @@ static int device_sms(int *sms) {
 }
 
 template <int NQ>
-static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, ChunkAttnParams p, int sms, cudaStream_t stream) {
+static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, ChunkAttnParams p, int sms,
+                        cudaStream_t stream) {
     const unsigned unit = NQ * p.slot_tokens;
     p.unit_inv = (unsigned)((0x100000000ull + unit - 1) / unit);
     const int grid = sms * Cfg<NQ>::kCtasPerSm;
@@ -1046,7 +1059,9 @@ extern "C" int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream) 
     const cuuint64_t qd[4] = {128, (cuuint64_t)Hq, (cuuint64_t)T, 1}, qs[3] = {256, tok, tok};
     const cuuint64_t pd[4] = {128, (cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)num_pages}, ps[3] = {256, page, page * Hkv};
     const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G), 1}, pb[4] = {64, (cuuint32_t)page_size, 1, 1};
-    if ((st = row_map(&tq, q, qd, qs, qb)) || (st = row_map(&tk, k_pool, pd, ps, pb)) || (st = row_map(&tv, v_pool, pd, ps, pb))) return st;
+    if ((st = row_map(&tq, q, qd, qs, qb))) return st;
+    if ((st = row_map(&tk, k_pool, pd, ps, pb))) return st;
+    if ((st = row_map(&tv, v_pool, pd, ps, pb))) return st;
     ChunkAttnParams p = {q,   k_pool, v_pool, q_stride,  page_table,        q_start,   ctx_len, out,  T,
                          B,   Hq,     Hkv,    page_size, max_pages_per_seq, num_pages, window,  scale};
     char *w = reinterpret_cast<char *>(ws);
