@@ -495,7 +495,8 @@ I4_API int decode_step_buffer_copy(i4_graph *g, int which, void *dev, size_t byt
 
 /*
  * Library options, applied to graphs created afterwards and to later calls:
- *   "pdl"    0/1 (default 1): launch the kernels of a decode step with programmatic
+ *   "pdl"    0/1 (default 1): launch the kernels of a decode step, and of the calls on
+ *            chunks and on the cache's pages, with programmatic
  *            dependent launch (each kernel still waits for its predecessor's
  *            results before reading them);
  *   "unpack" 0..4: INT4 unpack / multiply variant of the GEMV: 0 exact fp16

@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
     }
     if (warp == kLoadWarp && lane < 3)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &tm_q : (lane == 1 ? &tm_k : &tm_v)) : "memory");
+    grid_dep_wait();  // what the kernel before left: lengths, tables, q, the pages; and its use of the workspace has ended
     find_stretch<NQ>(p, &stretch, reinterpret_cast<int *>(gbase));
     fence_async_smem();  // its scratch lies where the first copy of Q will
     grid_dep_launch();  // the joining kernel may come up; it waits for this grid's end before it reads anything
@@ -856,6 +857,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
 template <int R>
 __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
     const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x;
+    grid_dep_launch();
     grid_dep_wait();
     const Cut c = p.cuts[first];
     if (!c.valid) return;
@@ -989,10 +991,11 @@ static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUte
     const unsigned unit = NQ * p.slot_tokens;
     p.unit_inv = (unsigned)((0x100000000ull + unit - 1) / unit);
     const int grid = sms * Cfg<NQ>::kCtasPerSm;
-    chunk_attn_kernel<NQ><<<grid, Cfg<NQ>::kThreads, Cfg<NQ>::kSmem, stream>>>(tq, tk, tv, p);
-    int st = launch_check("i4_paged_gqa_chunk");
+    const int st = cuda_check(launch(chunk_attn_kernel<NQ>, dim3(grid), dim3(Cfg<NQ>::kThreads), Cfg<NQ>::kSmem, stream, g_pdl, tq, tk,
+                                     tv, p),
+                              "i4_paged_gqa_chunk");
     if (st) return st;
-    return cuda_check(launch(chunk_join_kernel<Cfg<NQ>::kJoinRows>, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, true, p,
+    return cuda_check(launch(chunk_join_kernel<Cfg<NQ>::kJoinRows>, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, g_pdl, p,
                              (int)Cfg<NQ>::kUnitRows),
                       "i4_paged_gqa_chunk join");
 }

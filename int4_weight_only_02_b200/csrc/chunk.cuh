@@ -10,6 +10,10 @@
 
 namespace i4 {
 
+// The "pdl" option: the kernels of these calls start while the one before ends, and wait (grid_dep_wait) before they read or
+// write any memory.
+extern bool g_pdl;
+
 // The rows of sequence b, clamped to the T rows that exist: (first row, number of rows).
 __device__ __forceinline__ int2 chunk_rows(const int32_t *q_start, int b, int T) {
     const int a = min(max(q_start[b], 0), T), e = min(max(q_start[b + 1], 0), T);

@@ -14,6 +14,7 @@
 // bound by HBM. Three forks of a short sequence in 4 pools take 7.6 us, 63 of
 // one of 4015 tokens in 56 pools 22 us (12 to decide; 54 MB written), compacting
 // 9 pages of 4 pools 7 us, 300 pages of 56 pools 95 us (551 MB, 5.8 TB/s).
+#include "chunk.cuh"
 #include "common.cuh"
 
 namespace i4 {
@@ -109,6 +110,8 @@ __host__ __device__ inline Lists ws_lists(void *ws, size_t cap) {
 
 __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const CacheArgs c, const int32_t *seqs, const int32_t *add,
                                                                   int n, int32_t *status, Lists ws) {
+    grid_dep_launch();
+    grid_dep_wait();
     extern __shared__ int owner[];
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x;
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const CacheArg
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c, const int32_t *src, const int32_t *dst, int n,
                                                                int32_t *status, Lists ws, int smem_refs) {
     grid_dep_launch();  // the copy may come up; it waits for this kernel's end before it reads anything
+    grid_dep_wait();
     extern __shared__ int owner[];  // [S], then the counts of the pages where they fit
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -268,6 +272,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const CacheArgs c
 
 // One warp per sequence. The exchange makes a sequence that is named twice release its pages once.
 __global__ void kv_free_kernel(const CacheArgs c, const int32_t *seqs, int n) {
+    grid_dep_launch();
+    grid_dep_wait();
     const int i = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
     if (i >= n) return;
     const int s = seqs[i];
@@ -289,6 +295,7 @@ __global__ void kv_free_kernel(const CacheArgs c, const int32_t *seqs, int n) {
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(int32_t *refs, int num_pages, int32_t *n_live_out,
                                                                       Lists ws) {
     grid_dep_launch();
+    grid_dep_wait();
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x;
     int mine = 0, n_live;
@@ -354,6 +361,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
                                                                const int32_t *dst, int n, const int32_t *n_dev, int num_pages,
                                                                int page_vecs, int parts, const CacheArgs c, const int32_t *new_id,
                                                                int remap_blocks) {
+    grid_dep_launch();
     grid_dep_wait();
     if ((int)blockIdx.x < remap_blocks) {
         const int n_live = n_dev[1];
@@ -380,6 +388,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_rows_kernel(const __grid_constant__ PoolPtrs pools, const int32_t *from,
                                                                     const int32_t *to, const int32_t *fill, int n, int Hkv, int P,
                                                                     int row_vecs, int parts) {
+    grid_dep_launch();
     grid_dep_wait();
     const unsigned items = (unsigned)n * (unsigned)parts;
     for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
@@ -486,7 +495,7 @@ static int launch_copy(void *const *pools, int n_pools, const int32_t *src, cons
         }
         const dim3 grid(blocks + copy_grid((long long)n * parts, m), m);
         const int st = cuda_check(launch(kv_copy_kernel, grid, dim3(kCopyThreads), 0, stream,
-                                         n_dev != nullptr && p0 == 0, pp, src, dst, n, n_dev, num_pages, vecs, parts,
+                                         g_pdl, pp, src, dst, n, n_dev, num_pages, vecs, parts,
                                          remap ? *remap : CacheArgs{}, new_id, blocks),
                                   what);
         if (st) return st;
@@ -524,9 +533,9 @@ extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs
     if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_reserve: %d requests for %d sequences", n, cache->n_seqs);
     const size_t smem = (size_t)cache->n_seqs * sizeof(int);
     if ((st = plan_smem(kv_reserve_kernel, smem, "i4_kv_pages_reserve"))) return st;
-    kv_reserve_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), seqs, add, n, status,
-                                                                       ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs)));
-    return launch_check("i4_kv_pages_reserve");
+    return cuda_check(launch(kv_reserve_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), seqs,
+                             add, n, status, ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs))),
+                      "i4_kv_pages_reserve");
 }
 
 extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, const int32_t *src,
@@ -542,8 +551,10 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
     if (!smem_refs) smem = (size_t)cache->n_seqs * sizeof(int);
     if ((st = plan_smem(kv_fork_kernel, smem, "i4_kv_pages_fork"))) return st;
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
-    kv_fork_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(cache_args(cache), src, dst, n, status, L, smem_refs);
-    if ((st = launch_check("i4_kv_pages_fork"))) return st;
+    st = cuda_check(launch(kv_fork_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), src, dst,
+                           n, status, L, smem_refs),
+                    "i4_kv_pages_fork");
+    if (st) return st;
     const int row_vecs = D / 8, vecs = Hkv * cache->page_size * row_vecs;
     const int parts = (vecs + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
     for (int p0 = 0; p0 < n_pools; p0 += kPoolsPerLaunch) {
@@ -552,7 +563,7 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
         for (int i = 0; i < m; ++i) pp.p[i] = reinterpret_cast<unsigned char *>(pools[p0 + i]);
         const dim3 grid(copy_grid((long long)n * parts, m), m);
         st = cuda_check(launch(kv_copy_rows_kernel, grid, dim3(kCopyThreads), 0, (cudaStream_t)stream,
-                               p0 == 0, pp, (const int32_t *)L.b, (const int32_t *)L.c, (const int32_t *)L.c + n, n, Hkv,
+                               g_pdl, pp, (const int32_t *)L.b, (const int32_t *)L.c, (const int32_t *)L.c + n, n, Hkv,
                                cache->page_size, row_vecs, parts),
                         "i4_kv_pages_fork copy");
         if (st) return st;
@@ -564,8 +575,8 @@ extern "C" int i4_kv_pages_free(const i4_kv_cache *cache, const int32_t *seqs, i
     int st = check_cache("i4_kv_pages_free", cache);
     if (!st) st = check_list("i4_kv_pages_free", n, seqs, seqs);
     if (st || n == 0) return st;
-    kv_free_kernel<<<(n + 3) / 4, 128, 0, (cudaStream_t)stream>>>(cache_args(cache), seqs, n);
-    return launch_check("i4_kv_pages_free");
+    return cuda_check(launch(kv_free_kernel, dim3((n + 3) / 4), dim3(128), 0, (cudaStream_t)stream, g_pdl, cache_args(cache), seqs, n),
+                      "i4_kv_pages_free");
 }
 
 extern "C" int i4_kv_pages_compact(const i4_kv_cache *cache, void *const *pools, int n_pools, int Hkv, int D, int32_t *n_live, void *ws,
@@ -575,8 +586,10 @@ extern "C" int i4_kv_pages_compact(const i4_kv_cache *cache, void *const *pools,
     if (!st) st = check_ws("i4_kv_pages_compact", ws, ws_bytes, cache->num_pages, cache->n_seqs);
     if (st) return st;
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
-    kv_compact_plan_kernel<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(cache->refs, cache->num_pages, n_live, L);
-    if ((st = launch_check("i4_kv_pages_compact plan"))) return st;
+    st = cuda_check(launch(kv_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, g_pdl, cache->refs,
+                           cache->num_pages, n_live, L),
+                    "i4_kv_pages_compact plan");
+    if (st) return st;
     const CacheArgs args = cache_args(cache);
     return launch_copy(pools, n_pools, L.b, L.a, cache->num_pages, L.count, cache->num_pages,
                        (long long)Hkv * cache->page_size * D * 2, &args, L.c, (cudaStream_t)stream, "i4_kv_pages_compact");

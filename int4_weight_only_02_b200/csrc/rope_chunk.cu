@@ -53,6 +53,8 @@ struct RopeChunkParams {
 // rate). Eight single tokens take 3.1 us with the launch, a prompt of 512 4.6.
 template <bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int t = blockIdx.x;
     const int c = threadIdx.x & 15;  // 16-byte chunk of the head
     const int heads = p.Hq + 2 * p.Hkv, step = blockDim.x >> 4, h_first = threadIdx.x >> 4;
@@ -202,9 +204,7 @@ extern "C" int i4_rope_append_chunk(const i4_rope_chunk_args *args, void *stream
     int threads = 16 * ((Hq + 2 * Hkv + kRopeHeads - 1) / kRopeHeads);
     threads = (threads + 31) / 32 * 32;
     threads = threads > 512 ? 512 : threads;
-    if (interleaved)
-        rope_append_chunk_kernel<true, kRopeHeads><<<T, threads, 0, (cudaStream_t)stream>>>(p);
-    else
-        rope_append_chunk_kernel<false, kRopeHeads><<<T, threads, 0, (cudaStream_t)stream>>>(p);
-    return launch_check("i4_rope_append_chunk");
+    return cuda_check(launch(interleaved ? rope_append_chunk_kernel<true, kRopeHeads> : rope_append_chunk_kernel<false, kRopeHeads>,
+                             dim3(T), dim3(threads), 0, (cudaStream_t)stream, g_pdl, p),
+                      "i4_rope_append_chunk");
 }
