@@ -11,7 +11,7 @@
 //    tokens would. One TMA box of (64 dims, G heads, 128 / G tokens) brings half of a slot's Q in that order.
 //  * Work. A unit is NQ slots' tokens of one sequence and one kv head; its cost is the
 //    number of 128-position tiles that its rows see, and kUnitCost for beginning and ending it. The units stand in one line (kv
-//    heads outermost) and every CTA, one or two per SM, takes an equal stretch of the line: a prompt's long and short units
+//    heads outermost) and every CTA, one per SM, takes an equal stretch of the line: a prompt's long and short units
 //    balance, and a single token's long context spreads over the GPU. A unit that a border cuts leaves its parts
 //    (m, l, O) in the workspace and a second kernel joins them in order; a unit of at most kWhole tiles is not cut, since
 //    joining costs as much. The lengths are read on the device: every CTA finds its stretch by itself with two block-wide scans.
@@ -24,15 +24,17 @@
 //    follows the row's maximum when that is more than 2^8 ahead, so O is rarely rescaled (always following costs 20 %): P
 //    then reaches at most 2^8, far inside fp16. l and O are fp32.
 //  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
-//    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile and an SM; with
-//    NQ = 1, for chunks that fit one slot, two CTAs share an SM. (Whole tiles of 128 with the slots taking turns come out the same,
-//    254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.)
+//    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile; NQ = 1, for
+//    chunks that fit one slot, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an SM: four single
+//    tokens 15.6 us against 14.2, one at 32768 positions 32 against 26, 16 chunks of 16 at 3000 positions 44 against 37; both
+//    slots of a CTA on every other tile of one slot's rows: 15.7, 27 and 41). Whole tiles of 128 with the slots taking turns come out the
+//    same, 254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.
 //
 // Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows
 // costs 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the
 // clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a
 // steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 425 and 494 us. Few rows are bound by the chain of dependent
-// steps: four single tokens at up to 2049 positions take 16 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
+// steps: four single tokens at up to 2049 positions take 14 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
 // tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.
 #include <cmath>
 
@@ -48,15 +50,13 @@ constexpr int kTile = 128;                         // positions of a K/V tile
 constexpr unsigned kHalf = kTile * 128;            // 64 of the 128 dims of a tile, 128 bytes per row
 constexpr unsigned kTileBytes = 2 * kHalf;         // 32 KB
 constexpr int kStep = kTile / 2;                   // positions that a slot's softmax takes at once
-constexpr int kMaxCtas = 2 * kNumSMs;
 constexpr float kGrow = 8.f;                       // powers of two that a row's maximum may run ahead of its m
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NQ>
 struct Cfg {
     static constexpr int kThreads = NQ == 2 ? 384 : 192;  // softmax warpgroups, an MMA warp each, the load warps
-    static constexpr int kStages = NQ == 2 ? 5 : 2;
-    static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
+    static constexpr int kStages = NQ == 2 ? 5 : 6;
     static constexpr int kUnitRows = NQ * kRows;
     static constexpr int kUnitCost = 2;  // what beginning and ending a unit costs, in tiles
     static constexpr int kMinCost = 2;   // tiles that are worth a CTA of their own
@@ -85,7 +85,7 @@ struct ChunkAttnParams {
     float scale;
     int slot_tokens;      // 128 / G
     unsigned unit_inv;    // ceil(2^32 / (NQ * slot_tokens))
-    Cut *cuts;        // [kMaxCtas]
+    Cut *cuts;        // [CTAs]
     float2 *part_ml;  // [2 * CTAs][unit rows]: (m in powers of two, l)
     float *part_o;    // [2 * CTAs][unit rows][128]
 };
@@ -412,7 +412,7 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
 }
 
 template <int NQ>
-__global__ void __launch_bounds__(Cfg<NQ>::kThreads, Cfg<NQ>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkAttnParams p) {
     using C = Cfg<NQ>;
@@ -990,12 +990,11 @@ static int launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUte
                         cudaStream_t stream) {
     const unsigned unit = NQ * p.slot_tokens;
     p.unit_inv = (unsigned)((0x100000000ull + unit - 1) / unit);
-    const int grid = sms * Cfg<NQ>::kCtasPerSm;
-    const int st = cuda_check(launch(chunk_attn_kernel<NQ>, dim3(grid), dim3(Cfg<NQ>::kThreads), Cfg<NQ>::kSmem, stream, g_pdl, tq, tk,
+    const int st = cuda_check(launch(chunk_attn_kernel<NQ>, dim3(sms), dim3(Cfg<NQ>::kThreads), Cfg<NQ>::kSmem, stream, g_pdl, tq, tk,
                                      tv, p),
                               "i4_paged_gqa_chunk");
     if (st) return st;
-    return cuda_check(launch(chunk_join_kernel<Cfg<NQ>::kJoinRows>, dim3(grid, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, g_pdl, p,
+    return cuda_check(launch(chunk_join_kernel<Cfg<NQ>::kJoinRows>, dim3(sms, Cfg<NQ>::kUnitRows / 32), dim3(256), 0, stream, g_pdl, p,
                              (int)Cfg<NQ>::kUnitRows),
                       "i4_paged_gqa_chunk join");
 }
@@ -1012,13 +1011,12 @@ int read_chunk_error(int reset) {
     return v;
 }
 
-// Workspace: cuts | part_ml | part_o. Both variants have room for 2 * CTAs * unit rows = 4 * 148 * 128 rows.
-constexpr size_t kWsRows = (size_t)2 * kMaxCtas * kRows;
-constexpr size_t kWsMl = (kMaxCtas * sizeof(Cut) + 255) / 256 * 256;
+// Workspace: cuts | part_ml | part_o; two parts for every CTA, of the larger unit's rows.
+constexpr size_t kWsRows = (size_t)2 * kNumSMs * Cfg<2>::kUnitRows;
+constexpr size_t kWsMl = (kNumSMs * sizeof(Cut) + 255) / 256 * 256;
 constexpr size_t kWsO = kWsMl + kWsRows * sizeof(float2);
 constexpr size_t kWsBytes = kWsO + kWsRows * 128 * sizeof(float);
 static_assert(kWsO % 256 == 0, "parts are read 16 bytes at a time");
-static_assert(Cfg<1>::kUnitRows * Cfg<1>::kCtasPerSm == Cfg<2>::kUnitRows * Cfg<2>::kCtasPerSm, "one workspace size");
 
 }  // namespace i4
 
