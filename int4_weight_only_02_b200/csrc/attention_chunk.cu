@@ -16,7 +16,8 @@
 //    (m, l, O) in the workspace and a second kernel joins them in order; a unit of at most kWhole tiles is not cut, since
 //    joining costs as much. The lengths are read on the device: every CTA finds its stretch by itself with two block-wide scans.
 //  * Data. One warp loads K and V tiles (32 KB) page by page with TMA into a ring, 128-byte
-//    swizzled; a page outside the pools, or one that no row sees, is an
+//    swizzled (64 single tokens at 8000 positions: 5.6 TB/s with pages of 64, 4.2-4.7 with pages of 16, whose boxes of 2 KB
+//    are bound by the rate at which an SM's TMA takes them); a page outside the pools, or one that no row sees, is an
 //    out-of-range coordinate, which fills zeros.
 //  * Math. S = Q K^T (M = 128 rows, both operands K-major in shared memory) into tensor memory; the 128 threads of a
 //    warpgroup own one row each, so maximum and sum need no exchange; P = 2^(S - m), rounded to fp16 (the tensor cores'
@@ -25,17 +26,18 @@
 //    then reaches at most 2^8, far inside fp16. l and O are fp32.
 //  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
 //    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile; NQ = 1, for
-//    chunks that fit one slot, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an SM: four single
-//    tokens 15.6 us against 14.2, one at 32768 positions 32 against 26, 16 chunks of 16 at 3000 positions 44 against 37; both
-//    slots of a CTA on every other tile of one slot's rows: 15.7, 27 and 41). Whole tiles of 128 with the slots taking turns come out the
-//    same, 254 and 252 us on the case below: they load the tensor cores less but leave each slot waiting for its own product.
+//    chunks that fit one slot and for little work, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an
+//    SM: four single tokens 15.6 us against 14.2, one at 32768 positions 32 against 26, 16 chunks of 16 at 3000 positions 44
+//    against 37; both slots of a CTA on every other tile of one slot's rows: 15.7, 27 and 41). Whole tiles of 128 with the slots
+//    taking turns come out the same, 254 and 252 us on the case below: they load the tensor cores less but leave each slot
+//    waiting for its own product.
 //
 // Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows
 // costs 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the
 // clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a
 // steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 425 and 494 us. Few rows are bound by the chain of dependent
 // steps: four single tokens at up to 2049 positions take 14 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
-// tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 19 us.
+// tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 17 us.
 #include <cmath>
 
 #include "chunk.cuh"
@@ -1070,8 +1072,13 @@ extern "C" int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream) 
     p.part_ml = reinterpret_cast<float2 *>(w + kWsMl);
     p.part_o = reinterpret_cast<float *>(w + kWsO);
     p.slot_tokens = kRows / G;
-    // one slot of 128 rows when every chunk fits it: the other warpgroup would idle
+    // One slot of 128 rows when every chunk fits it: the other warpgroup would idle. Also when units of one slot find an SM each
+    // and have a few tiles only: a slot alone takes a tile in 1.3 us, two in 1.9, and the kernel begins and ends sooner. (28
+    // heads on 4, 512 tokens at 512 positions: 17.0 us against 19.6, at 1024: 26.5 and 26.0, at 2048: 38.4 against 32.5; 256
+    // tokens: 13.4 against 16.0, 21.4 against 23.0, 27.7 against 25.7.)
     const int longest = max_q > 0 && max_q < T ? max_q : T;
-    if (longest <= p.slot_tokens) return launch_chunk<1>(tq, tk, tv, p, sms, (cudaStream_t)stream);
+    const long long units = ((long long)(T + p.slot_tokens - 1) / p.slot_tokens + B) * Hkv;  // at most
+    const bool few = units <= sms && (long long)max_pages_per_seq * page_size <= 1024;
+    if (longest <= p.slot_tokens || few) return launch_chunk<1>(tq, tk, tv, p, sms, (cudaStream_t)stream);
     return launch_chunk<2>(tq, tk, tv, p, sms, (cudaStream_t)stream);
 }

@@ -12,6 +12,19 @@ pytestmark = pytest.mark.gpu
 SENTINEL = 77.0
 
 
+EMPTY = 0
+
+
+@pytest.fixture(params=[0, 150], ids=["", "wide"], autouse=True)
+def empty_sequences(request):
+    """Every test runs as it is, and with 150 sequences without tokens behind its own (short prompts are worked on in units of one
+    slot where the GPU has an SM for each, else of two)."""
+    global EMPTY
+    EMPTY = request.param
+    yield
+    EMPTY = 0
+
+
 def case(lens, hq, hkv, page, seed, pad=0, width=None):
     rng = np.random.default_rng(seed)
     k, v, table = cc.paged(lens, hkv, page, rng, width=width)
@@ -22,6 +35,8 @@ def case(lens, hq, hkv, page, seed, pad=0, width=None):
 def call(i4, cuda, q, k, v, table, lens, **kw):
     import torch
     out = torch.full(q.shape, SENTINEL, dtype=torch.float16, device=cuda)
+    lens = list(lens) + [(0, 0)] * EMPTY
+    table = np.concatenate([table, np.full((EMPTY, table.shape[1]), -1, dtype=np.int32)])
     i4.paged_gqa_chunk(dev(q, cuda), dev(k, cuda), dev(v, cuda), dev(table, cuda), dev(cc.starts(lens), cuda),
                        dev(np.array([c for _, c in lens], dtype=np.int32), cuda), out=out, **kw)
     torch.cuda.synchronize()
@@ -68,6 +83,18 @@ def test_many_sequences(i4lib, cuda, n_seq):
     lens = [(int(a), int(a + b)) for a, b in zip(rng.integers(0, 3, n_seq), rng.integers(0, 40, n_seq))]
     q, k, v, table = case(lens, 4, 2, 8, seed=n_seq, pad=2)
     check(call(i4lib, cuda, q, k, v, table, lens, max_q=2), q, k, v, table, lens, 8)
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (7, 1, [(700, 4000), (40, 3000), (19, 6001), (37, 900), (1, 5000), (36, 2500)]),
+    (40, 20, [(200, 200), (130, 700), (65, 70), (64, 64)]),
+    (12, 12, [(300, 300), (129, 130), (128, 1000), (257, 400)]),
+])
+def test_units_of_two_slots(i4lib, cuda, hq, hkv, lens, window):
+    """Too much for units of one slot: units whose second slot is full, has a token or has none."""
+    q, k, v, table = case(lens, hq, hkv, 32, seed=hq + window, pad=3)
+    check(call(i4lib, cuda, q, k, v, table, lens, window=window), q, k, v, table, lens, 32, window)
 
 
 @pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 300, 5000])
