@@ -94,11 +94,15 @@ struct ChunkAttnParams {
 
 // ------------------------------------------------------------------ the line of units
 
+// The first position that the token at pos sees.
+__device__ __forceinline__ int first_seen(const ChunkAttnParams &p, int pos) {
+    return p.window > 0 ? max(0, max(pos, 0) - (p.window - 1)) : 0;  // no overflow at positions below 0 and windows up to 2^31 - 1
+}
+
 // Positions that the tokens [a, e) of a sequence whose first new token stands at pos0 may see: [x, y), empty when y <= x.
 __device__ __forceinline__ int2 seen(const ChunkAttnParams &p, int pos0, int a, int e) {
     const int hi = min(pos0 + e, p.max_pages * p.page_size);
-    const int lo = p.window > 0 ? max(0, pos0 + a - p.window + 1) : 0;
-    return make_int2(lo, hi);
+    return make_int2(first_seen(p, pos0 + a), hi);
 }
 __device__ __forceinline__ int2 tiles_of(int2 s) {
     return s.y > s.x ? make_int2(s.x / kTile, (s.y + kTile - 1) / kTile) : make_int2(0, 0);
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
         auto limits = [&](const Piece &c, int &lo, int &hi) {  // positions that this thread's row sees
             const int pos = c.pos0 + c.tok0 + s * p.slot_tokens + my_tok;
             hi = min(pos + 1, p.max_pages * p.page_size);
-            lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            lo = first_seen(p, pos);
         };
         auto finish = [&](const Piece &last, const int3 &last_r) {
             if (last_r.z == 0) return;  // the slot has no rows

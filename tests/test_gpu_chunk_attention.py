@@ -104,6 +104,14 @@ def test_window(i4lib, cuda, window):
     check(call(i4lib, cuda, q, k, v, table, lens, window=window), q, k, v, table, lens, 16, window)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_widest_window(i4lib, cuda, window):
+    """Also where a chunk begins at negative positions: the window's first position stays a number of 32 bits."""
+    lens = [(40, 10), (1, 300), (9, 9), (200, 150)]
+    q, k, v, table = case([(40, 40), (1, 300), (9, 9), (200, 200)], 7, 1, 16, seed=12)
+    check(call(i4lib, cuda, q, k, v, table, lens, window=window), q, k, v, table, lens, 16)
+
+
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, 65504.0])
 def test_what_a_row_does_not_see_does_not_reach_it(i4lib, cuda, bad):
     """K and V of later tokens of the chunk, and of tokens before the window, hold NaN or infinity: the rows that do not
