@@ -242,7 +242,9 @@ I4_API int i4_argmax_rows(const float *logits, int32_t *tokens, int32_t *pos, in
  *   q_start   [B + 1] int32 device array, not decreasing: rows q_start[b] ..
  *             q_start[b + 1] - 1 of the call's T rows are the new tokens of
  *             sequence b (none when both are equal). Rows from q_start[B] on
- *             belong to nobody and their outputs are left as they were.
+ *             belong to nobody and their outputs are left as they were. (One that
+ *             does decrease, or points outside the rows, is followed within the call's rows only:
+ *             rows that no sequence or several name get anyone's result or none.)
  *   ctx_len   [B] int32 device array: tokens of sequence b INCLUDING the new
  *             ones, so new token i of n stands at position ctx_len[b] - n + i.
  *   page_table, page_size, max_pages_per_seq as for paged_gqa_decode;

@@ -265,7 +265,7 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
         if (off_end >= 0) atomicAdd(&out->left, off_end - (target_end - at));
     };
     for (int pass = 0; pass < 2; ++pass) {  // the first measures the line, the second finds the place in it
-        int run = 0, trips = 0;
+        int run = 0, trips = 0, all_units = 0;
         for (int b0 = 0; b0 < p.B; b0 += NT) {
             int n = 0, first_pos = 0, total_units;
             if (b0 + tid < p.B) {
@@ -273,6 +273,12 @@ __device__ __forceinline__ void find_stretch(const ChunkAttnParams &p, Stretch *
                 first_pos = max(p.ctx_len[b0 + tid], 0) - n;
             }
             const int before = scan_block<NT>(units_of<NQ>(p, n), total_units, sums);
+            all_units += total_units;
+            // a q_start that decreases has sequences share rows: not as many as would make the line longer than its ints hold
+            if (all_units > units_of<NQ>(p, p.T) + p.B) {
+                run = 0;
+                break;
+            }
             first[tid] = before;
             tokens[tid] = n;
             pos[tid] = first_pos;

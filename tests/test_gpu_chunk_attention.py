@@ -249,6 +249,25 @@ def test_captured_call_follows_the_lengths(i4lib, cuda):
         check(out.cpu().numpy(), q, k, v, table, lens, 16)
 
 
+@pytest.mark.parametrize("starts", [[0, 500, 0, 500], [0, 500] * 20, [500, 0] * 450, [0, 300, 200] + [500] * 30,
+                                    [-5, 100, 2 ** 31 - 1, -2 ** 31, 400]])
+def test_starts_that_decrease_stay_within_the_rows(i4lib, cuda, starts):
+    """Sequences that claim the same rows, or rows that do not exist: whatever comes of it, nothing is written behind the rows and
+    the next call is right."""
+    import torch
+    T, n_seq = 500, len(starts) - 1
+    lens = [(T, 600)]
+    q, k, v, table = case(lens, 7, 1, 16, seed=31)
+    buf = torch.full((T + 64, *q.shape[1:]), SENTINEL, dtype=torch.float16, device=cuda)
+    ctx = torch.full((n_seq,), 600, dtype=torch.int32, device=cuda)
+    i4lib.paged_gqa_chunk(dev(q, cuda), dev(k, cuda), dev(v, cuda), dev(np.tile(table, (n_seq, 1)), cuda),
+                          dev(np.array(starts, dtype=np.int32), cuda), ctx, out=buf[:T])
+    torch.cuda.synchronize()
+    assert i4lib.device_error() == 0
+    assert (buf[T:] == SENTINEL).all()
+    check(call(i4lib, cuda, q, k, v, table, lens), q, k, v, table, lens, 16)
+
+
 def test_two_streams_with_their_own_workspaces(i4lib, cuda):
     import torch
     sets = []
