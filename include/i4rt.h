@@ -315,7 +315,7 @@ I4_API int i4_rope_append_chunk(const i4_rope_chunk_args *args, void *stream);
  *   ws     workspace of i4_paged_gqa_chunk_ws_bytes() bytes (the same for every
  *          shape), 256-byte aligned, with any contents. Calls sharing one ws must not overlap on the GPU.
  * Requires D == 128, Hq % Hkv == 0, Hq / Hkv <= 8, page_size a power of two in
- * [8, 128], scale > 0, T <= 2^20, B <= 65536, max_pages_per_seq * page_size <= 2^20.
+ * [8, 128], 0 < scale <= 1e20, T <= 2^20, B <= 65536, max_pages_per_seq * page_size <= 2^20.
  */
 I4_API size_t i4_paged_gqa_chunk_ws_bytes(void);
 typedef struct i4_chunk_attn_args {

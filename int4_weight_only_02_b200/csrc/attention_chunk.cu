@@ -1053,7 +1053,8 @@ extern "C" int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream) 
     // a CTA's share of the line of tiles is counted in 31 bits
     if ((double)Hkv * (T / (kRows / (Hq / Hkv)) + (double)B) * ((double)max_pages_per_seq * page_size / kTile + 3) > 1e11)
         return fail(I4_EUNSUPPORTED, "i4_paged_gqa_chunk: T, B, Hkv and the page-table row are too large together");
-    if (!(scale > 0.f) || std::isinf(scale)) return fail(I4_EINVAL, "i4_paged_gqa_chunk: scale %g must be positive", scale);
+    // |q . k| is at most 128 * 65504^2 = 5.5e11: a scaled score stays a finite float
+    if (!(scale > 0.f) || scale > 1e20f) return fail(I4_EINVAL, "i4_paged_gqa_chunk: scale %g must be positive, at most 1e20", scale);
     if (q_stride < (long long)Hq * D || q_stride % 8)
         return fail(I4_EINVAL, "i4_paged_gqa_chunk: q_stride %lld must be >= Hq*D and a multiple of 8", q_stride);
     if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || !aligned(page_table, 4) ||

@@ -30,7 +30,7 @@ ATTN = [("q", FAKE), ("q_stride", 28 * 128), ("k", FAKE), ("v", FAKE), ("table",
     (dict(pages=0), -1), (dict(window=-1), -1), (dict(max_q=-1), -1), (dict(D=64), -3), (dict(Hq=30, q_stride=30 * 128), -3),
     (dict(Hq=36, q_stride=36 * 128), -3), (dict(page=4), -3), (dict(page=24), -3), (dict(page=256), -3), (dict(T=(1 << 20) + 1), -3),
     (dict(B=65537), -3), (dict(max_pages=1 << 17), -3), (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=float("nan")), -1),
-    (dict(scale=float("inf")), -1), (dict(q_stride=28 * 128 - 8), -1), (dict(q_stride=28 * 128 + 4), -1), (dict(q=FAKE + 8), -2),
+    (dict(scale=float("inf")), -1), (dict(scale=1e21), -1), (dict(q_stride=28 * 128 - 8), -1), (dict(q_stride=28 * 128 + 4), -1), (dict(q=FAKE + 8), -2),
     (dict(k=FAKE + 8), -2), (dict(v=FAKE + 2), -2), (dict(out=FAKE + 8), -2), (dict(table=FAKE + 2), -2), (dict(q_start=FAKE + 1), -2),
     (dict(T=1 << 20, B=65536, Hkv=4096, Hq=4096, q_stride=4096 * 128, max_pages=1 << 16, ws_bytes=1 << 40), -3),
     (dict(ws=None), -1), (dict(), -1), (dict(ws_bytes=1 << 40, ws=FAKE + 16), -2),
