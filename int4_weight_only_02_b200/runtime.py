@@ -444,10 +444,11 @@ class Prefill:
         return seq.token
 
 
-def _int_list(v, dev):
-    """A device int32 tensor of a host sequence or tensor."""
+def _int_list(v, dev, stream):
+    """A device int32 tensor of a host sequence or tensor, made (and given back) on the stream of the call that reads it."""
     import torch
-    return torch.as_tensor(v, dtype=torch.int32).to(dev)
+    with torch.cuda.stream(stream):  # None: the current one
+        return torch.as_tensor(v, dtype=torch.int32).to(dev)
 
 
 class PagedCache:
@@ -476,19 +477,19 @@ class PagedCache:
         """Room for add[i] more tokens of sequence seqs[i], whose length grows by it; status [n] (see kv_pages_reserve)."""
         from . import kv_pages_reserve
         dev = self.refs.device
-        return kv_pages_reserve(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, dev),
-                                _int_list(add, dev), ws=self.ws, stream=stream)
+        return kv_pages_reserve(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, dev, stream),
+                                _int_list(add, dev, stream), ws=self.ws, stream=stream)
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] continues src[i]; status [n] (see kv_pages_fork)."""
         from . import kv_pages_fork
         dev = self.refs.device
-        return kv_pages_fork(self.pools, self.page_table, self.ctx_len, self.refs, _int_list(src, dev), _int_list(dst, dev),
-                             ws=self.ws, stream=stream)
+        return kv_pages_fork(self.pools, self.page_table, self.ctx_len, self.refs, _int_list(src, dev, stream),
+                             _int_list(dst, dev, stream), ws=self.ws, stream=stream)
 
     def free(self, seqs, stream=None):
         from . import kv_pages_free
-        kv_pages_free(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, self.refs.device),
+        kv_pages_free(self.page_table, self.ctx_len, self.refs, self.page_size, _int_list(seqs, self.refs.device, stream),
                       stream=stream)
 
     def compact(self, stream=None):

@@ -95,6 +95,23 @@ def test_no_pages_leaves_the_cache_as_it_was(i4lib, cuda, parts, model):
     text.feed(dec, {0: [nxt[0]], 2: prompt[:40]})
 
 
+def test_cache_calls_on_a_stream_that_is_behind(i4lib, cuda, model):
+    """The lists that a call makes of its arguments live until its stream has read them."""
+    import torch
+    cache = i4lib.PagedCache(model, n_seqs=6, num_pages=40)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    status = [cache.reserve([3, 1, 0], [20, 16, 33], stream=side), cache.fork([3, 1], [2, 4], stream=side)]
+    cache.free([1], stream=side)
+    over = [torch.full((k,), -7, dtype=torch.int32, device=cuda) for k in (1, 2, 3) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert [s.cpu().tolist() for s in status] == [[0, 0, 0], [0, 0]] and len(over) == 24
+    assert cache.ctx_len.cpu().tolist() == [33, 0, 20, 20, 16, 0]
+    assert [len(row[row >= 0]) for row in cache.page_table.cpu()] == [3, 0, 2, 2, 1, 0]
+
+
 def test_refusals(i4lib, cuda, model):
     cache = i4lib.PagedCache(model, n_seqs=2, num_pages=20)
     dec = i4lib.ChunkedDecoder(model, cache, max_tokens=16)
