@@ -514,6 +514,12 @@ class ChunkedDecoder:
         import torch
         from . import paged_gqa_chunk_ws_bytes, rope_table
         s, dev = model.shape, model.device
+        P, row = s.page_size, cache.max_pages * s.page_size
+        if P not in (8, 16, 32, 64, 128) or s.head_dim != 128 or s.n_q % s.n_kv or s.n_q // s.n_kv > 8 or row > 1 << 20:
+            raise ValueError(f"ChunkedDecoder: pages of {P}, {s.n_q} heads of {s.head_dim} on {s.n_kv} and page-table rows of {row} "
+                             "positions are not served (see paged_gqa_chunk)")
+        if not 1 <= int(max_tokens) <= 65535:
+            raise ValueError(f"ChunkedDecoder: max_tokens {max_tokens} (1 to 65535)")
         self.model, self.cache, self.shape = model, cache, s
         self.n_max = n = int(max_tokens)
         f16 = dict(dtype=torch.float16, device=dev)

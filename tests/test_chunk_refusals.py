@@ -166,3 +166,16 @@ def test_python_calls_refuse_what_they_could_not_follow(i4lib):
         i4lib.kv_pages_reserve(table, ctx, refs, 16, seq, seq)
     with pytest.raises(i4lib.I4Error, match="int32"):
         i4lib.kv_pages_free(table, ctx.long(), refs, 16, seq)
+
+
+@pytest.mark.parametrize("change,max_tokens", [
+    (dict(page_size=24), 16), (dict(page_size=256), 16), (dict(n_q=9, n_kv=1), 16), (dict(n_q=7, n_kv=2), 16), (dict(head_dim=64), 16),
+    (dict(page_size=16, max_pages=65537), 16), (dict(), 0), (dict(), 65536),
+])
+def test_decoder_over_what_its_calls_do_not_take(i4lib, change, max_tokens):
+    """Refused when it is made, not by a call in the middle of a run, whose reservation would stay."""
+    from types import SimpleNamespace
+    d = dict(dict(page_size=16, n_q=4, n_kv=2, head_dim=128, max_pages=4), **change)
+    cache = SimpleNamespace(max_pages=d.pop("max_pages"))
+    with pytest.raises(ValueError, match="ChunkedDecoder"):
+        i4lib.ChunkedDecoder(SimpleNamespace(shape=SimpleNamespace(**d), device="cpu"), cache, max_tokens)
