@@ -27,7 +27,7 @@
 //  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
 //    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile; NQ = 1, for
 //    chunks that fit one slot and for little work, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an
-//    SM: four single tokens 15.6 us against 14.2, one at 32768 positions 32 against 26, 16 chunks of 16 at 3000 positions 44
+//    SM: four single tokens 15.6 us against 14.7, one at 32768 positions 32 against 26, 16 chunks of 16 at 3000 positions 44
 //    against 37; both slots of a CTA on every other tile of one slot's rows: 15.7, 27 and 41). Whole tiles of 128 with the slots
 //    taking turns come out the same, 254 and 252 us on the case below: they load the tensor cores less but leave each slot
 //    waiting for its own product.
@@ -37,7 +37,7 @@
 // clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a
 // steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 425 and 494 us. Few rows are bound by the chain of dependent
 // steps: four single tokens at up to 2049 positions take 14 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
-// tile, 1.2 to store a part and 4 to join them; a prompt of 512 takes 17 us.
+// tile, 1.2 to store a part and 3.5 to join them; a prompt of 512 takes 17 us.
 #include <cmath>
 
 #include "chunk.cuh"
@@ -62,8 +62,8 @@ struct Cfg {
     static constexpr int kUnitRows = NQ * kRows;
     static constexpr int kUnitCost = 2;  // what beginning and ending a unit costs, in tiles
     static constexpr int kMinCost = 2;   // tiles that are worth a CTA of their own
-    // rows of a warp of the joining kernel, out of eight loads in flight: the few rows of short chunks come in many parts
-    // (four single tokens: 16.0 us with 2, 16.8 with 4), full tiles in two or three (a mixed batch: 52.1 and 48.6 us)
+    // rows of a warp of the joining kernel, out of eight loads in flight: the rows of short chunks come in many parts
+    // (16 chunks of 16: 37.3 us with 2, 40.0 with 1), full tiles in two or three (a mixed batch: 49.5 us with 4, 52 with 2)
     static constexpr int kJoinRows = NQ == 2 ? 4 : 2;
     static constexpr int kWhole = 4;     // a unit of at most so many tiles is not cut: joining would take longer
     static constexpr unsigned kTmemCols = NQ * 256;  // S / P and O of every slot
@@ -864,15 +864,11 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
 }
 
 // The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
-// Grid (CTAs of the main kernel, blocks of 32 rows); a warp has R rows at once, lane = four columns. The weights of 32 parts are in
-// the lanes at once and eight loads are in flight, so the kernel costs a few latencies (it is bound by nothing else).
+// A warp has R rows at once, lane = four columns. The weights of 32 parts are in the lanes at once and eight loads are in
+// flight.
 template <int R>
-__global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
-    const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv, first = blockIdx.x;
-    grid_dep_launch();
-    grid_dep_wait();
-    const Cut c = p.cuts[first];
-    if (!c.valid) return;
+__device__ __forceinline__ void join_rows(const ChunkAttnParams &p, const Cut &c, int G, int unit_rows) {
+    const int lane = threadIdx.x & 31, first = blockIdx.x;
     const int parts = c.last - first + 2;
     const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
     constexpr int U = 8 / R;  // parts of each of a warp's R rows that are in flight together
@@ -952,6 +948,22 @@ __global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constan
             *reinterpret_cast<uint2 *>(p.out + ((size_t)(c.row + tok) * p.Hq + hq) * 128 + 4 * lane) = h;
         }
     }
+}
+
+// Grid (CTAs of the main kernel, blocks of 32 rows). The kernel costs a few latencies and is bound by nothing else, so a unit
+// of at most eight rows has one a warp, with eight parts in flight (four single tokens: 14.2 us against 14.7 with two
+// rows, one at 32768 positions 24.1 against 26.3).
+template <int R>
+__global__ void __launch_bounds__(256, 3) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p, int unit_rows) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const Cut c = p.cuts[blockIdx.x];
+    const int G = p.Hq / p.Hkv;
+    if (!c.valid) return;
+    if (c.tokens * G <= 8)
+        join_rows<1>(p, c, G, unit_rows);
+    else
+        join_rows<R>(p, c, G, unit_rows);
 }
 
 // ------------------------------------------------------------------ host side

@@ -50,7 +50,7 @@ struct RopeChunkParams {
 // (sequence, position, page and angles) for few: the first heads' values, which depend on none of it, are loaded first.
 // A thread takes kHeads heads at once; finding the token's place costs it as much as two or three of them (16397 tokens of
 // 36 heads, half of each rotated, 306 MB: 56 us with two, issue slots 77 % busy; 50 us with four, 6.2 TB/s, 95 % of the copy
-// rate). Eight single tokens take 3.1 us with the launch, a prompt of 512 4.6.
+// rate). Eight single tokens take 3.4 us with the launch, a prompt of 512 5.1.
 template <bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(512) rope_append_chunk_kernel(const RopeChunkParams p) {
     grid_dep_wait();
