@@ -304,7 +304,8 @@ I4_API int i4_rope_append_chunk(const i4_rope_chunk_args *args, void *stream);
  * The token at position p of sequence b sees the positions t <= p, and only
  * t > p - window when window > 0; for query head h and kv head g = h / (Hq / Hkv)
  *   out = sum_t softmax_t(scale * q . K[g][t]) V[g][t]      (fp32 sums, fp16 out)
- * P = exp(s - m) is rounded to fp16 before it meets V. A token that sees
+ * P, 2^7 to 2^15 at its largest, is rounded to fp16 before it meets V: each weight by 2^-11 of itself, or by 2^-32 of
+ * the row's largest weight where that is more. A token that sees
  * nothing (a negative position) gives zeros; positions behind the page-table row
  * are not seen. What lies in a page outside a token's positions, NaN included,
  * does not reach its output.

@@ -20,10 +20,12 @@
 //    are bound by the rate at which an SM's TMA takes them); a page outside the pools, or one that no row sees, is an
 //    out-of-range coordinate, which fills zeros.
 //  * Math. S = Q K^T (M = 128 rows, both operands K-major in shared memory) into tensor memory; the 128 threads of a
-//    warpgroup own one row each, so maximum and sum need no exchange; P = 2^(S - m), rounded to fp16 (the tensor cores'
-//    operand type; 2^-11 of each weight), goes back over S's columns and is the A operand of O += P V (V MN-major). m only
+//    warpgroup own one row each, so maximum and sum need no exchange; P = 2^(S - m + 7), rounded to fp16 (the tensor cores'
+//    operand type), goes back over S's columns and is the A operand of O += P V (V MN-major). m only
 //    follows the row's maximum when that is more than 2^8 ahead, so O is rarely rescaled (always following costs 20 %): P
-//    then reaches at most 2^8, far inside fp16. l and O are fp32.
+//    then reaches at most 2^15, inside fp16. The rounding is 2^-11 of a weight down to 2^-21 of the row's largest, where P
+//    becomes subnormal, and 2^-32 of the largest below that; without the 7, which costs nothing and cancels in O / l, a sink's
+//    tail of 2^20 positions at 2^-25 of it would be lost to P V, though not to l. l and O are fp32.
 //  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
 //    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile; NQ = 1, for
 //    chunks that fit one slot and for little work, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an
@@ -53,6 +55,7 @@ constexpr unsigned kHalf = kTile * 128;            // 64 of the 128 dims of a ti
 constexpr unsigned kTileBytes = 2 * kHalf;         // 32 KB
 constexpr int kStep = kTile / 2;                   // positions that a slot's softmax takes at once
 constexpr float kGrow = 8.f;                       // powers of two that a row's maximum may run ahead of its m
+constexpr float kLift = 7.f;                       // powers of two that P, l and O are held above the weights: at most 2^15 for P
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NQ>
@@ -390,7 +393,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 // right already. A lane has the score of one position of 32, then four dims of the sum over them (some 25 cycles a position, so
 // that a row of 2^20 positions stays far inside the other warps' waits).
 __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g, const uint16_t *q, int lo, int hi, float qs,
-                                         float m_scaled) {
+                                         float m_lift) {
     const int lane = threadIdx.x & 31;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int u0 = lo; u0 < hi; u0 += 32) {
@@ -407,7 +410,7 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
                 s = fma2_f16_f32(a.z, x.z, s);
                 s = fma2_f16_f32(a.w, x.w, s);
             }
-        const float w = ex2(fmaf(s, qs, -m_scaled));
+        const float w = ex2(fmaf(s, qs, m_lift));
         const unsigned rows = __ballot_sync(0xffffffffu, there);
 #pragma unroll 8
         for (int k = 0; k < 32; ++k) {
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (mk > -INFINITY)
                     v = plain_row(p, last.b, last.g, p.q + (size_t)(last.row0 + tk) * p.q_stride + (size_t)hk * 128, lo, hi, qs,
-                                  mk * qs);
+                                  fmaf(-mk, qs, kLift));
                 if (last.whole) {
                     uint16_t *d = p.out + ((size_t)(last.row0 + tk) * p.Hq + hk) * 128 + 4 * lane;
                     d[0] = float_to_half_bits(v.x * inv);
@@ -826,7 +829,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
                         }
                     }
                 }
-                const float mm = m == -INFINITY ? 0.f : -m * qs;
+                const float mm = m == -INFINITY ? 0.f : fmaf(-m, qs, kLift);
                 const float2 mm2 = make_float2(mm, mm), qs2 = make_float2(qs, qs);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
