@@ -25,7 +25,10 @@
 //    follows the row's maximum when that is more than 2^8 ahead, so O is rarely rescaled (always following costs 20 %): P
 //    then reaches at most 2^15, inside fp16. The rounding is 2^-11 of a weight down to 2^-21 of the row's largest, where P
 //    becomes subnormal, and 2^-32 of the largest below that; without the 7, which costs nothing and cancels in O / l, a sink's
-//    tail of 2^20 positions at 2^-25 of it would be lost to P V, though not to l. l and O are fp32.
+//    tail of 2^20 positions at 2^-25 of it would be lost to P V, though not to l. l and O are fp32. The exponent is one FMA,
+//    s c - (m c - 7) with c = scale log2(e), whose second term is rounded: by 2^-15 at most while m c is below 1000, but by
+//    more than any exponent for the largest scores. A row whose m passes that counts its scores from m on, in the branches that
+//    mask and that move the maximum: one more for it costs 8 to 10 %.
 //  * Overlap. A slot takes a tile in two halves of 64 positions: while its threads compute one half's exponentials, the tensor
 //    cores run the other half's P V and the next tile's S over it. With NQ = 2 two slots share every tile; NQ = 1, for
 //    chunks that fit one slot and for little work, has a deeper ring instead (two CTAs of one slot and two tiles of ring on an
@@ -56,6 +59,7 @@ constexpr unsigned kTileBytes = 2 * kHalf;         // 32 KB
 constexpr int kStep = kTile / 2;                   // positions that a slot's softmax takes at once
 constexpr float kGrow = 8.f;                       // powers of two that a row's maximum may run ahead of its m
 constexpr float kLift = 7.f;                       // powers of two that P, l and O are held above the weights: at most 2^15 for P
+constexpr float kFar = 1000.f;                     // size of a row's m, in powers of two, from which scores count from there
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NQ>
@@ -91,7 +95,7 @@ struct ChunkAttnParams {
     int slot_tokens;      // 128 / G
     unsigned unit_inv;    // ceil(2^32 / (NQ * slot_tokens))
     Cut *cuts;        // [CTAs]
-    float2 *part_ml;  // [2 * CTAs][unit rows]: (m in powers of two, l)
+    float2 *part_ml;  // [2 * CTAs][unit rows]: (m, l), m a score before the scale
     float *part_o;    // [2 * CTAs][unit rows][128]
 };
 
@@ -388,20 +392,25 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
     }
 }
 
-// The sum over the positions [lo, hi) of one row by plain loads, for rows whose tensor-core sum met a NaN or an
-// infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. The row's m and l are
-// right already. A lane has the score of one position of 32, then four dims of the sum over them (some 25 cycles a position, so
-// that a row of 2^20 positions stays far inside the other warps' waits).
-__device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g, const uint16_t *q, int lo, int hi, float qs,
-                                         float m_lift) {
+// The softmax sums of one row over the positions [lo, hi) by plain loads, for rows whose tensor-core sum met a NaN or an
+// infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. Returns O, and (m, l) in
+// `ml`: its scores are sums in another order than the tensor cores', so it has a maximum of its own. A lane has the score
+// of one position of 32, then four dims of the sum over them (some 25 cycles a position, so that a row of 2^20 positions
+// stays far inside the other warps' waits).
+struct PlainRow {
+    float4 o;
+    float2 ml;
+};
+__device__ __noinline__ PlainRow plain_row(const ChunkAttnParams &p, int b, int g, const uint16_t *q, int lo, int hi, float qs) {
     const int lane = threadIdx.x & 31;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
     for (int u0 = lo; u0 < hi; u0 += 32) {
         const int u = u0 + lane;
         const int page = u < hi ? p.page_table[(size_t)b * p.max_pages + u / p.page_size] : -1;
         const bool there = page >= 0 && page < p.num_pages;  // else K and V are zeros
         const size_t off = there ? (((size_t)page * p.Hkv + g) * p.page_size + u % p.page_size) * 128 : 0;
-        float s = 0.f;
+        float s = u < hi ? 0.f : -INFINITY;
         if (there)
             for (int c = 0; c < 128; c += 8) {
                 const uint4 a = *reinterpret_cast<const uint4 *>(p.k_pool + off + c), x = *reinterpret_cast<const uint4 *>(q + c);
@@ -410,7 +419,17 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
                 s = fma2_f16_f32(a.z, x.z, s);
                 s = fma2_f16_f32(a.w, x.w, s);
             }
-        const float w = ex2(fmaf(s, qs, m_lift));
+        float mx = s;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        if (mx > m) {
+            const float alpha = ex2((m - mx) * qs);
+            m = mx;
+            l *= alpha;
+            o = make_float4(o.x * alpha, o.y * alpha, o.z * alpha, o.w * alpha);
+        }
+        const float w = m == -INFINITY ? 0.f : ex2(fmaf(s - m, qs, kLift));
+        l += w;
         const unsigned rows = __ballot_sync(0xffffffffu, there);
 #pragma unroll 8
         for (int k = 0; k < 32; ++k) {
@@ -423,7 +442,7 @@ __device__ __noinline__ float4 plain_row(const ChunkAttnParams &p, int b, int g,
             o = make_float4(fmaf(wk, a.x, o.x), fmaf(wk, a.y, o.y), fmaf(wk, c.x, o.z), fmaf(wk, c.y, o.w));
         }
     }
-    return o;
+    return {o, make_float2(m, warp_sum(l))};
 }
 
 template <int NQ>
@@ -654,6 +673,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
         bool ok = true;
 
         float m = -INFINITY, l = 0.f;
+        float ref = 0.f;  // m and the scores count from here: 0, or a score of this row once those are far from 0
         auto limits = [&](const Piece &c, int &lo, int &hi) {  // positions that this thread's row sees
             const int pos = c.pos0 + c.tok0 + s * p.slot_tokens + my_tok;
             hi = min(pos + 1, p.max_pages * p.page_size);
@@ -668,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
             float *part = p.part_o + (size_t)(slot_row & ~3) * 128 + 4 * (lane & 3);  // the first row of this group of four lanes
             const int my_rows = min(max(last_r.z * G - (row & ~3), 0), 4);
             if (!last.whole && mine)  // an all-NaN row has l = NaN and no maximum: keep it from reading as empty
-                p.part_ml[slot_row] = make_float2(l != l ? 0.f : (m == -INFINITY ? m : m * qs), l);
+                p.part_ml[slot_row] = make_float2(l != l ? 0.f : m + ref, l);
             if (any) {
                 ok = wait_or_stop(&pv_done[s][0], (tiles - 1) & 1, stop) && wait_or_stop(&pv_done[s][1], (tiles - 1) & 1, stop);
                 ok = __all_sync(0xffffffffu, ok);
@@ -755,20 +775,22 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
                 limits(last, lo, hi);
                 lo = max(__shfl_sync(0xffffffffu, lo, k), last_r.x * kTile);
                 hi = min(__shfl_sync(0xffffffffu, hi, k), last_r.y * kTile);
-                const float mk = __shfl_sync(0xffffffffu, m, k), inv = __shfl_sync(0xffffffffu, l_inv, k);
                 const int tk = __shfl_sync(0xffffffffu, tok, k), hk = __shfl_sync(0xffffffffu, head, k);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (mk > -INFINITY)
-                    v = plain_row(p, last.b, last.g, p.q + (size_t)(last.row0 + tk) * p.q_stride + (size_t)hk * 128, lo, hi, qs,
-                                  fmaf(-mk, qs, kLift));
+                const PlainRow pr =
+                    plain_row(p, last.b, last.g, p.q + (size_t)(last.row0 + tk) * p.q_stride + (size_t)hk * 128, lo, hi, qs);
+                const float4 v = pr.o;
+                const float2 ml = pr.ml;
                 if (last.whole) {
+                    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                     uint16_t *d = p.out + ((size_t)(last.row0 + tk) * p.Hq + hk) * 128 + 4 * lane;
                     d[0] = float_to_half_bits(v.x * inv);
                     d[1] = float_to_half_bits(v.y * inv);
                     d[2] = float_to_half_bits(v.z * inv);
                     d[3] = float_to_half_bits(v.w * inv);
                 } else {
-                    reinterpret_cast<float4 *>(p.part_o)[((size_t)last.slot * C::kUnitRows + s * kRows + 32 * wq + k) * 32 + lane] = v;
+                    const int at = last.slot * C::kUnitRows + s * kRows + 32 * wq + k;
+                    reinterpret_cast<float4 *>(p.part_o)[(size_t)at * 32 + lane] = v;
+                    if (lane == k) p.part_ml[at] = ml;  // the lane that wrote it before
                 }
             }
         };
@@ -777,6 +799,7 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
             const int3 r = slot_tiles(p, pc, s);
             m = -INFINITY;
             l = 0.f;
+            ref = 0.f;
             int lo, hi;
             limits(pc, lo, hi);
             if (my_tok >= r.z) {  // no row: anything goes, nothing is stored
@@ -795,10 +818,10 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
                 tmem_wait_ld32(x);
                 tmem_wait_ld32(x + 32);
                 const int a = lo - u * kStep, e = hi - u * kStep;  // the row sees [a, e) of these positions
-                if (__any_sync(0xffffffffu, a > 0 || e < kStep)) {
+                if (__any_sync(0xffffffffu, a > 0 || e < kStep || ref != 0.f)) {
 #pragma unroll
                     for (int i = 0; i < kStep; ++i)
-                        if (i < a || i >= e) x[i] = 0xff800000u;  // -inf
+                        x[i] = i < a || i >= e ? 0xff800000u /* -inf */ : __float_as_uint(__uint_as_float(x[i]) - ref);
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -809,8 +832,20 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
                     mx3 = max3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
                 }
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                const bool up = mx > m + grow;
+                const bool up = mx - m > grow;  // m + grow would be rounded by more than grow where m is large
                 if (__any_sync(0xffffffffu, up)) {
+                    const bool far = up && fabsf(mx * qs) >= kFar;
+                    if (__any_sync(0xffffffffu, far)) {
+                        // count from the maximum (what rounding leaves of it is a step of it at most, and nothing the next time)
+                        // and take the half again
+                        if (far) {
+                            const float to = ref + mx;
+                            m += ref - to;
+                            ref = to;
+                        }
+                        --u;
+                        continue;
+                    }
                     const float alpha = up ? ex2((m - mx) * qs) : 1.f;  // 0 for a row that had seen nothing
                     if (up) m = mx;
                     l *= alpha;
@@ -866,12 +901,14 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1)
     }
 }
 
-// The parts of the units that the stretches cut: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, in the order of k.
+// The parts of the units that the stretches cut: out = sum_k w_k O_k / sum_k w_k l_k, w_k = 2^((m_k - M) scale log2(e)), in the
+// order of k.
 // A warp has R rows at once, lane = four columns. The weights of 32 parts are in the lanes at once and eight loads are in
 // flight.
 template <int R>
 __device__ __forceinline__ void join_rows(const ChunkAttnParams &p, const Cut &c, int G, int unit_rows) {
     const int lane = threadIdx.x & 31, first = blockIdx.x;
+    const float qs = p.scale * kLog2e;
     const int parts = c.last - first + 2;
     const auto slot = [&](int k) { return k == 0 ? 2 * first - 1 : 2 * (first + k - 1); };  // the k-th part's
     constexpr int U = 8 / R;  // parts of each of a warp's R rows that are in flight together
@@ -912,7 +949,7 @@ __device__ __forceinline__ void join_rows(const ChunkAttnParams &p, const Cut &c
             unsigned there[R];  // parts that saw something: the others have no O
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                w[i] = ml[i].x > -INFINITY ? exp2f(ml[i].x - M[i]) : 0.f;
+                w[i] = ml[i].x > -INFINITY ? exp2f((ml[i].x - M[i]) * qs) : 0.f;
                 L[i] += warp_sum(w[i] * ml[i].y);
                 there[i] = __ballot_sync(0xffffffffu, ml[i].x > -INFINITY);
             }
