@@ -14,6 +14,8 @@
 // bound by HBM. Three forks of a short sequence in 4 pools take 7.6 us, 63 of
 // one of 4015 tokens in 56 pools 22 us (12 to decide; 54 MB written), compacting
 // 9 pages of 4 pools 7 us, 300 pages of 56 pools 95 us (551 MB, 5.8 TB/s).
+#include <mutex>
+
 #include "chunk.cuh"
 #include "common.cuh"
 
@@ -466,12 +468,30 @@ static CacheArgs cache_args(const i4_kv_cache *c) {
 
 // The plan kernels keep an int per sequence, and the fork one per page too where they fit, in dynamic shared memory: many
 // targets of one source count the same pages up and down, and 63 of them over 251 pages took 17 us on global atomics. The
-// attribute that allows more than 48 KB belongs to the current device, and setting it again costs little beside a launch.
+// attribute that allows more than 48 KB belongs to the kernel on the device, whoever calls it: it is set once, to the most
+// that any call takes.
 constexpr size_t kPlanSmem = 200 * 1024;
-template <typename K>
-static int plan_smem(K kernel, size_t bytes, const char *what) {
-    if (bytes <= 47 * 1024) return I4_OK;
-    return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what);
+static_assert(kMaxSeqs * sizeof(int) <= kPlanSmem, "the table of owners always fits");
+
+constexpr int kMaxDevices = 64;
+struct PlanState {
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+};
+
+static int plan_smem(const char *what) {
+    static PlanState state[kMaxDevices];
+    int dev = 0;
+    const int st = cuda_check(cudaGetDevice(&dev), what);
+    if (st) return st;
+    if (dev < 0 || dev >= kMaxDevices) return fail(I4_EUNSUPPORTED, "%s: device %d", what, dev);
+    PlanState &d = state[dev];
+    std::call_once(d.once, [&] {
+        d.err = cudaFuncSetAttribute(kv_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPlanSmem);
+        if (d.err == cudaSuccess)
+            d.err = cudaFuncSetAttribute(kv_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPlanSmem);
+    });
+    return d.err == cudaSuccess ? I4_OK : cuda_check(d.err, what);
 }
 
 // Blocks along x for `items` work items in each of m pools: enough for the whole GPU, and no more than there are items.
@@ -532,7 +552,7 @@ extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs
     if (st || n == 0) return st;
     if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_reserve: %d requests for %d sequences", n, cache->n_seqs);
     const size_t smem = (size_t)cache->n_seqs * sizeof(int);
-    if ((st = plan_smem(kv_reserve_kernel, smem, "i4_kv_pages_reserve"))) return st;
+    if ((st = plan_smem("i4_kv_pages_reserve"))) return st;
     return cuda_check(launch(kv_reserve_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), seqs,
                              add, n, status, ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs))),
                       "i4_kv_pages_reserve");
@@ -549,7 +569,7 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
     size_t smem = ((size_t)cache->n_seqs + cache->num_pages) * sizeof(int);
     const int smem_refs = smem <= kPlanSmem;
     if (!smem_refs) smem = (size_t)cache->n_seqs * sizeof(int);
-    if ((st = plan_smem(kv_fork_kernel, smem, "i4_kv_pages_fork"))) return st;
+    if ((st = plan_smem("i4_kv_pages_fork"))) return st;
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
     st = cuda_check(launch(kv_fork_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), src, dst,
                            n, status, L, smem_refs),

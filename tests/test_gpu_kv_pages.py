@@ -1,4 +1,6 @@
 """Copying, reserving, forking, freeing and compacting pages against plain Python (needs a B200); every comparison is of bits."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -250,4 +252,43 @@ def test_captured_operations(i4lib, cuda):
         g.replay()
         c.model.reserve([0], [3])
         c.model.fork([0], [1])
+        c.same()
+
+
+def test_two_threads_with_caches_of_different_sizes(i4lib, cuda):
+    """Each thread has its own cache, workspace and stream. The plans of both need more shared memory than a kernel has without
+    asking, one three times the other's. The calls follow each other as fast as a host can make them, so that they meet."""
+    import threading
+    import torch
+    errors, both = [], threading.Barrier(2)
+
+    def work(c, num_pages):
+        stream = torch.cuda.Stream()
+        ws = torch.empty(i4lib.kv_pages_ws_bytes(num_pages, 30), dtype=torch.uint8, device=cuda)
+        src, dst, status = c.ints([0, 0]), c.ints([1, 2]), c.ints([7, 7])
+        desc = i4lib.KvCacheDesc(c.table.data_ptr(), c.ctx.data_ptr(), c.refs.data_ptr(), 30, 20, 8, num_pages)
+        pools = (ctypes.c_void_p * 1)(c.pools[0].data_ptr())
+        fork = i4lib.lib().i4_kv_pages_fork
+        args = (ctypes.byref(desc), pools, 1, 1, 8, src.data_ptr(), dst.data_ptr(), 2, status.data_ptr(), ws.data_ptr(), ws.numel(),
+                stream.cuda_stream)
+        torch.cuda.synchronize()
+        both.wait()
+        for _ in range(4000):
+            st = fork(*args)
+            if st:
+                errors.append((num_pages, st, i4lib.lib().i4_last_error()))
+                return
+
+    caches = [Both(i4lib, cuda, 30, 20, 8, n, n_pools=1, d=8) for n in (13000, 40000)]
+    for c in caches:
+        c.reserve([0], [13])
+    threads = [threading.Thread(target=work, args=(c, len(c.model.refs))) for c in caches]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for c in caches:
+        c.model.fork([0, 0], [1, 2])
         c.same()
