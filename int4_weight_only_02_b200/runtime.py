@@ -545,9 +545,10 @@ class ChunkedDecoder:
     def run(self, chunks: dict, stream=None):
         """Feeds chunks[seq] (token ids, at least one) to every sequence named; returns (next tokens [len(chunks)] int32,
         logits [len(chunks)][vocab] fp32) of their last tokens, in ascending order of the sequences. Raises I4Error, with
-        nothing fed, when a sequence's pages do not suffice (which reads the reservation's status from the device)."""
+        nothing fed, when there are not enough free pages (I4_ENOMEM) or a sequence would be longer than its page-table row
+        (I4_EINVAL, whatever is free); both are read from the device, as the reservation's status."""
         import torch
-        from . import (I4_ENOMEM, I4Error, argmax_rows, embed_gather, int4_gemm, paged_gqa_chunk, rmsnorm, rope_append_chunk,
+        from . import (I4_EINVAL, I4_ENOMEM, I4Error, argmax_rows, embed_gather, int4_gemm, paged_gqa_chunk, rmsnorm, rope_append_chunk,
                        silu_mul)
         m, s, cache = self.model, self.shape, self.cache
         g, L, dev = m.glob, m.layers, m.device
@@ -565,9 +566,13 @@ class ChunkedDecoder:
             before = cache.ctx_len.clone()
             status = cache.reserve(seqs, lens[seqs], stream=st)
             if int(status.max().item()):
-                bad = [k for k, v in zip(seqs, status.tolist()) if v]
-                # what was granted is given back: lengths first, then the pages behind them
-                self._give_back(before, st)
+                status = status.tolist()
+                self._give_back(before, st)  # what was granted
+                bad = [k for k, v in zip(seqs, status) if v == 2]
+                if bad:
+                    raise I4Error(I4_EINVAL, f"ChunkedDecoder.run: {lens[bad].tolist()} tokens more are too many for sequences {bad}, "
+                                             f"whose page-table rows hold {cache.max_pages * cache.page_size} positions")
+                bad = [k for k, v in zip(seqs, status) if v]
                 raise I4Error(I4_ENOMEM, f"ChunkedDecoder.run: no pages for {lens[bad].tolist()} tokens of sequences {bad}")
             start = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(dev)
             last = torch.from_numpy((np.cumsum(lens[seqs]) - 1).astype(np.int32)).to(dev)

@@ -135,3 +135,29 @@ def test_extended_context(i4lib, cuda, parts, model):
         got.append(logits[0].cpu().numpy())
     assert normwise_err(got[1], got[0]) <= 1e-2
     assert normwise_err(got[0], oracle_logits(parts, prompt)) > 1e-2
+
+
+def state_of(cache):
+    return [t.cpu().numpy() for t in (cache.page_table, cache.ctx_len, cache.refs)]
+
+
+def same_state(cache, state):
+    for a, b in zip(state, state_of(cache)):
+        assert np.array_equal(a, b)
+
+
+def test_more_tokens_than_the_row_holds(i4lib, cuda, parts, model):
+    """Not a lack of pages: freeing some would not help, so it is another error; what was granted is given back."""
+    cache = i4lib.PagedCache(model, n_seqs=3, num_pages=30, max_pages_per_seq=3)
+    dec = i4lib.ChunkedDecoder(model, cache, max_tokens=64)
+    text = Text(parts)
+    prompt = synth.prompt_tokens(SHAPE, 60, seed=4)
+    nxt = text.feed(dec, {0: prompt[:47], 1: prompt[:5]})
+    text.feed(dec, {0: [nxt[0]]})  # the row is full
+    state = state_of(cache)
+    for chunks in ({0: [1]}, {0: [1], 1: prompt[:20], 2: [3]}, {2: prompt[:49]}):
+        with pytest.raises(i4lib.I4Error, match="48 positions") as e:
+            dec.run(chunks)
+        assert e.value.status == i4lib.I4_EINVAL
+        same_state(cache, state)
+    text.feed(dec, {1: [nxt[1]], 2: prompt[:48]})
