@@ -546,12 +546,10 @@ class ChunkedDecoder:
         """Feeds chunks[seq] (token ids, at least one) to every sequence named; returns (next tokens [len(chunks)] int32,
         logits [len(chunks)][vocab] fp32) of their last tokens, in ascending order of the sequences. Raises I4Error, with
         nothing fed, when there are not enough free pages (I4_ENOMEM) or a sequence would be longer than its page-table row
-        (I4_EINVAL, whatever is free); both are read from the device, as the reservation's status."""
+        (I4_EINVAL, whatever is free), both read from the device as the reservation's status, or as any call of the pass does."""
         import torch
-        from . import (I4_EINVAL, I4_ENOMEM, I4Error, argmax_rows, embed_gather, int4_gemm, paged_gqa_chunk, rmsnorm, rope_append_chunk,
-                       silu_mul)
-        m, s, cache = self.model, self.shape, self.cache
-        g, L, dev = m.glob, m.layers, m.device
+        from . import I4_EINVAL, I4_ENOMEM, I4Error
+        cache = self.cache
         seqs = sorted(int(k) for k in chunks)
         toks = [np.asarray(chunks[k], dtype=np.int32).reshape(-1) for k in seqs]
         lens = np.zeros(cache.n_seqs, dtype=np.int32)
@@ -574,36 +572,49 @@ class ChunkedDecoder:
                                              f"whose page-table rows hold {cache.max_pages * cache.page_size} positions")
                 bad = [k for k, v in zip(seqs, status) if v]
                 raise I4Error(I4_ENOMEM, f"ChunkedDecoder.run: no pages for {lens[bad].tolist()} tokens of sequences {bad}")
-            start = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(dev)
-            last = torch.from_numpy((np.cumsum(lens[seqs]) - 1).astype(np.int32)).to(dev)
-            tokens = torch.from_numpy(np.concatenate(toks)).to(dev)
-            r, xn, qkv, q, attn, y, gu, mlp = (t[:n] for t in (self.r, self.xn, self.qkv, self.q, self.attn, self.y, self.gu,
-                                                               self.mlp))
-            flat, longest = attn.view(n, -1), int(lens.max())
-            embed_gather(g["embed"], tokens, r, stream=st)
-            rmsnorm(r, L[0]["ln_in"], out=xn, eps=s.eps, stream=st)
-            for li, lw in enumerate(L):
-                int4_gemm(lw["w_qkv"], lw["s_qkv"], xn, lw["b_qkv"], y=qkv, ws=self.gemm_ws, stream=st)
-                rope_append_chunk(qkv, start, cache.ctx_len, self.cs, s.n_q, s.n_kv, cache.k_pools[li], cache.v_pools[li],
-                                  cache.page_table, q_out=q, stream=st)
-                paged_gqa_chunk(q, cache.k_pools[li], cache.v_pools[li], cache.page_table, start, cache.ctx_len, out=attn,
-                                max_q=longest, ws=self.attn_ws, stream=st)
-                int4_gemm(lw["w_o"], lw["s_o"], flat, y=y, ws=self.gemm_ws, stream=st)
-                rmsnorm(y, lw["ln_post"], out=xn, resid=r, eps=s.eps, stream=st)
-                int4_gemm(lw["w_gu"], lw["s_gu"], xn, y=gu, ws=self.gemm_ws, stream=st)
-                silu_mul(gu, out=mlp, stream=st)
-                int4_gemm(lw["w_d"], lw["s_d"], mlp, y=y, ws=self.gemm_ws, stream=st)
-                gamma = L[li + 1]["ln_in"] if li + 1 < len(L) else g["ln_final"]
-                rmsnorm(y, gamma, out=xn, resid=r, eps=s.eps, stream=st)
-            ends = torch.empty((len(seqs), s.hidden), dtype=torch.float16, device=dev)
-            embed_gather(xn, last, ends, stream=st)
-            logits = int4_gemm(g["w_lm"], g["s_lm"], ends, out_fp32=True, ws=self.gemm_ws, stream=st)
-            out = torch.empty(len(seqs), dtype=torch.int32, device=dev)
-            argmax_rows(logits, out, stream=st)
+            try:
+                return self._feed(seqs, toks, lens, st)
+            except BaseException:
+                self._give_back(before, st)  # what was enqueued before the failure wrote behind these lengths alone
+                raise
+
+    def _feed(self, seqs, toks, lens, st):
+        """The pass over the new tokens of `seqs`, whose pages are reserved; the current stream is st."""
+        import torch
+        from . import argmax_rows, embed_gather, int4_gemm, paged_gqa_chunk, rmsnorm, rope_append_chunk, silu_mul
+        m, s, cache, n = self.model, self.shape, self.cache, int(lens.sum())
+        g, L, dev = m.glob, m.layers, m.device
+        start = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(dev)
+        last = torch.from_numpy((np.cumsum(lens[seqs]) - 1).astype(np.int32)).to(dev)
+        tokens = torch.from_numpy(np.concatenate(toks)).to(dev)
+        r, xn, qkv, q, attn, y, gu, mlp = (t[:n] for t in (self.r, self.xn, self.qkv, self.q, self.attn, self.y, self.gu,
+                                                           self.mlp))
+        flat, longest = attn.view(n, -1), int(lens.max())
+        embed_gather(g["embed"], tokens, r, stream=st)
+        rmsnorm(r, L[0]["ln_in"], out=xn, eps=s.eps, stream=st)
+        for li, lw in enumerate(L):
+            int4_gemm(lw["w_qkv"], lw["s_qkv"], xn, lw["b_qkv"], y=qkv, ws=self.gemm_ws, stream=st)
+            rope_append_chunk(qkv, start, cache.ctx_len, self.cs, s.n_q, s.n_kv, cache.k_pools[li], cache.v_pools[li],
+                              cache.page_table, q_out=q, stream=st)
+            paged_gqa_chunk(q, cache.k_pools[li], cache.v_pools[li], cache.page_table, start, cache.ctx_len, out=attn,
+                            max_q=longest, ws=self.attn_ws, stream=st)
+            int4_gemm(lw["w_o"], lw["s_o"], flat, y=y, ws=self.gemm_ws, stream=st)
+            rmsnorm(y, lw["ln_post"], out=xn, resid=r, eps=s.eps, stream=st)
+            int4_gemm(lw["w_gu"], lw["s_gu"], xn, y=gu, ws=self.gemm_ws, stream=st)
+            silu_mul(gu, out=mlp, stream=st)
+            int4_gemm(lw["w_d"], lw["s_d"], mlp, y=y, ws=self.gemm_ws, stream=st)
+            gamma = L[li + 1]["ln_in"] if li + 1 < len(L) else g["ln_final"]
+            rmsnorm(y, gamma, out=xn, resid=r, eps=s.eps, stream=st)
+        ends = torch.empty((len(seqs), s.hidden), dtype=torch.float16, device=dev)
+        embed_gather(xn, last, ends, stream=st)
+        logits = int4_gemm(g["w_lm"], g["s_lm"], ends, out_fp32=True, ws=self.gemm_ws, stream=st)
+        out = torch.empty(len(seqs), dtype=torch.int32, device=dev)
+        argmax_rows(logits, out, stream=st)
         return out, logits
 
     def _give_back(self, before, st):
-        """After a reservation that was granted in part: the lengths as they were before, and the pages behind them free."""
+        """After a reservation that was granted in part, or a pass that failed: the lengths as they were before, and the pages
+        behind them free."""
         import torch
         cache, P = self.cache, self.cache.page_size
         place = torch.arange(cache.max_pages, device=before.device)

@@ -161,3 +161,24 @@ def test_more_tokens_than_the_row_holds(i4lib, cuda, parts, model):
         assert e.value.status == i4lib.I4_EINVAL
         same_state(cache, state)
     text.feed(dec, {1: [nxt[1]], 2: prompt[:48]})
+
+
+@pytest.mark.parametrize("at", ["embed_gather", "rope_append_chunk", "silu_mul", "argmax_rows"])
+def test_a_call_that_fails_leaves_the_cache_as_it_was(i4lib, cuda, parts, model, monkeypatch, at):
+    cache = i4lib.PagedCache(model, n_seqs=3, num_pages=30)
+    dec = i4lib.ChunkedDecoder(model, cache, max_tokens=64)
+    text = Text(parts)
+    prompt = synth.prompt_tokens(SHAPE, 60, seed=5)
+    nxt = text.feed(dec, {0: prompt[:30], 2: prompt[:17]})
+    state = state_of(cache)
+
+    def fails(*a, **kw):
+        raise i4lib.I4Error(i4lib.I4_EINVAL, "made to fail")
+
+    with monkeypatch.context() as m:
+        m.setattr(i4lib, at, fails)
+        with pytest.raises(i4lib.I4Error, match="made to fail"):
+            dec.run({0: [nxt[0]], 1: prompt[:33], 2: [1, 2, 3]})
+    same_state(cache, state)
+    nxt = text.feed(dec, {0: [nxt[0]], 1: prompt[:33], 2: [nxt[2]]})
+    text.feed(dec, {k: [nxt[k]] for k in range(3)})
