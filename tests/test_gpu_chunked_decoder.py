@@ -182,3 +182,13 @@ def test_a_call_that_fails_leaves_the_cache_as_it_was(i4lib, cuda, parts, model,
     same_state(cache, state)
     nxt = text.feed(dec, {0: [nxt[0]], 1: prompt[:33], 2: [nxt[2]]})
     text.feed(dec, {k: [nxt[k]] for k in range(3)})
+
+
+def test_a_cache_of_another_model_is_refused(i4lib, cuda, model, parts):
+    import dataclasses
+    for change in (dict(page_size=8), dict(layers=1), dict(n_kv=4)):
+        other = dataclasses.replace(SHAPE, **change)
+        weights = [synth.layer_weights(other, i, 4) for i in range(other.layers)], synth.global_weights(other, 4)
+        cache = i4lib.PagedCache(i4lib.DeviceModel(other, *weights, device=cuda), n_seqs=2, num_pages=8)
+        with pytest.raises(ValueError, match="cache"):
+            i4lib.ChunkedDecoder(model, cache, max_tokens=16)
