@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 import struct
 
@@ -481,8 +482,12 @@ def paged_gqa_chunk(q, k_pool, v_pool, page_table, q_start, ctx_len, out=None, w
     return out
 
 
+_SHAPE = operator.attrgetter("shape")
+
+
 def _pool_array(name: str, pools):
-    """(host array of the pools' addresses, shape of the first) of a sequence of equal pools of 16-bit values."""
+    """(host array of the pools' addresses, their shape) of a sequence of pools of 16-bit values and one layout: pages of another
+    would be moved by the first one's."""
     import torch
     T = torch.Tensor
     shape = pools[0].shape if len(pools) else ()
@@ -491,9 +496,9 @@ def _pool_array(name: str, pools):
     dev = pools[0].get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         _refuse(name, f"pools on the current CUDA device are needed, got {pools[0].device}")
-    if (set(map(T.numel, pools)) != {pools[0].numel()} or set(map(T.element_size, pools)) != {2}
+    if (list(map(_SHAPE, pools)) != [shape] * len(pools) or set(map(T.element_size, pools)) != {2}
             or not all(map(T.is_contiguous, pools)) or set(map(T.get_device, pools)) != {dev}):
-        _refuse(name, "pools of one size, two bytes a value, contiguous and on one device are needed")
+        _refuse(name, "pools of one shape, two bytes a value, contiguous and on one device are needed")
     return array.array("Q", map(T.data_ptr, pools)), shape
 
 

@@ -292,3 +292,21 @@ def test_two_threads_with_caches_of_different_sizes(i4lib, cuda):
     for c in caches:
         c.model.fork([0, 0], [1, 2])
         c.same()
+
+
+@pytest.mark.parametrize("calls", ["copy", "fork", "compact"])
+def test_pools_of_different_layouts_are_refused(i4lib, cuda, calls):
+    """The same number of values, but other pages, heads or rows: one call cannot move both."""
+    import torch
+    c = Both(i4lib, cuda, 4, 3, 8, 6, n_pools=2, hkv=2, d=16)
+    c.reserve([0], [11])
+    for shape in ((6, 1, 8, 32), (6, 4, 4, 16), (12, 1, 8, 16), (6, 2, 16, 8)):
+        pools = [c.pools[0], torch.zeros(shape, dtype=torch.float16, device=cuda)]
+        with pytest.raises(i4lib.I4Error, match="one shape"):
+            if calls == "copy":
+                i4lib.kv_pages_copy(pools, c.ints([0]), c.ints([5]))
+            elif calls == "fork":
+                i4lib.kv_pages_fork(pools, c.table, c.ctx, c.refs, c.ints([0]), c.ints([1]))
+            else:
+                i4lib.kv_pages_compact(pools, c.table, c.ctx, c.refs)
+    c.same()
