@@ -339,7 +339,8 @@ I4_API int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream);
  * K and V pools: one call moves a page in all of them).
  *
  * refs[p] counts the sequences that hold page p (0 = free; a caller keeps a page out
- * of the cache by counting it itself). Sequence s holds page_table[s][0 ..
+ * of the cache by counting it itself: one of the lowest ids if it ever compacts, since those never move,
+ * where another page in use may, and no table would tell). Sequence s holds page_table[s][0 ..
  * ceil(ctx_len[s] / page_size)); a page that is not full has one holder. Pages
  * are handed out lowest id first, in the order of the requests, so the same
  * calls give the same pages.
@@ -352,7 +353,8 @@ I4_API int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream);
  *                        held is given back, src's full pages are shared, and the filled rows of a
  *                        last page that is not full are copied to a new page.
  *   i4_kv_pages_free     the sequences' pages are given back, ctx_len = 0, rows -1
- *                        (ids outside [0, n_seqs) are skipped; naming one twice is harmless).
+ *                        (ids outside [0, n_seqs) are skipped; naming one twice is harmless; the row of a
+ *                        sequence without tokens is left as it is).
  *   i4_kv_pages_compact  moves the n_live pages in use to ids 0 .. n_live - 1: the
  *                        j-th free id below n_live takes the j-th used page at or above it;
  *                        refs and page_table follow. n_live (device, or NULL) gets the count.

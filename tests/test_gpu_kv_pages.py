@@ -310,3 +310,19 @@ def test_pools_of_different_layouts_are_refused(i4lib, cuda, calls):
             else:
                 i4lib.kv_pages_compact(pools, c.table, c.ctx, c.refs)
     c.same()
+
+
+def test_pages_that_the_caller_counts_itself(i4lib, cuda):
+    """Held out of the cache at the lowest ids they are never handed out, and compaction leaves them where they are."""
+    c = Both(i4lib, cuda, 4, 6, 8, 30)
+    c.model.refs[:3] = 1
+    c.upload()
+    before = [p[:3].copy() for p in c.model.pools]
+    c.reserve([0, 1, 2], [20, 30, 9])
+    c.fork([1], [3])
+    c.free([0, 1])
+    assert c.compact() == 3 + 2 + 4
+    c.free([2, 3])
+    assert c.compact() == 3
+    for p, b in zip(c.pools, before):
+        assert np.array_equal(p[:3].cpu().numpy().view(np.uint16), b)
