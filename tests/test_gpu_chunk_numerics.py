@@ -1,5 +1,5 @@
-"""Attention of new tokens where its numbers are hard: weights far below the row's largest, scores of any finite size
-(needs a B200)."""
+"""Attention of new tokens where its numbers are hard: weights far below the row's largest, scores of any finite size, rows
+summed again in parts of a cut unit, the longest row (needs a B200)."""
 import numpy as np
 import pytest
 
@@ -159,6 +159,39 @@ def test_a_maximum_that_creeps_at_large_scores(i4lib, cuda):
         assert np.all(got[0, h] >= near.min(0) - slack) and np.all(got[0, h] <= near.max(0) + slack)
 
 
+# ------------------------------------------------------------------ rows summed again in parts of a cut unit
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, 65504.0])
+@pytest.mark.parametrize("lens,window", [
+    ([(5, 20005)], 0), ([(40, 20040)], 0), ([(5, 20005)], 3000), ([(40, 9040), (5, 20005), (1, 700)], 2500),
+    ([(60, 30000), (200, 12200)], 4000),
+])
+def test_what_a_row_does_not_see_in_a_cut_unit(i4lib, cuda, bad, lens, window):
+    """Long contexts whose units are cut into parts: K and V of the last token, and of the tokens just before the last row's
+    window, are NaN or infinite. Rows that see none of them are held to the bound, and no page lies in order."""
+    rng = np.random.default_rng(len(lens) + window)
+    k, v, table = cc.paged(lens, 1, 64, rng)
+    q = rng.standard_normal((int(cc.starts(lens)[-1]), 7, cc.D)).astype(np.float16)
+    clean, good, row = (k.copy(), v.copy()), [], 0
+    for b, (n, ctx) in enumerate(lens):
+        marked = {ctx - 1}
+        if window:  # seen by the chunk's first row, not by the later ones; the first sees nothing else that is marked
+            marked |= {ctx - n - window + 1} if ctx - n - window + 1 >= 0 else set()
+        for t in marked:
+            put(k, table, b, t, bad)
+            put(v, table, b, t, bad)
+        for i in range(n):
+            pos = ctx - n + i
+            if not any(t <= pos and (not window or t > pos - window) for t in marked):
+                good.append(row + i)
+        row += n
+    got = call(i4lib, cuda, q, k, v, table, lens, window=window)
+    want, bound = cc.attention(q, *clean, table, lens, 64, window)
+    assert len(good) >= len(q) - 2 * len(lens)
+    off = np.abs(got[good] - want[good]) - bound[good]
+    assert np.all(np.isfinite(got[good])) and off.max() <= 0, off.max()
+
+
 def test_rows_summed_again_beside_large_scores(i4lib, cuda):
     """Scores of 2^30 and a NaN in the last token's V: the other rows are summed again and still give their largest's V."""
     for n, ctx in ((3, 700), (6, 9000), (300, 1300)):
@@ -168,3 +201,88 @@ def test_rows_summed_again_beside_large_scores(i4lib, cuda):
         got = call(i4lib, cuda, q, k, v, table, lens)[:-1]
         assert np.all(np.isfinite(got))
         assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -10 + 2.0 ** -13) + 2.0 ** -25)
+
+
+# ------------------------------------------------------------------ the longest row
+
+def longest_row(q, k, v, keep=None):
+    """64-bit attention of q [Hq][128] over k, v, with what an fp16 result may be off: A and the weights from the reference
+    itself. `keep` drops positions."""
+    import torch
+    s = q.double() @ k.double().T / np.sqrt(cc.D)
+    if keep is not None:
+        s = s.masked_fill(~keep, -float("inf"))
+    p = torch.softmax(s, dim=1)
+    out, a = p @ v.double(), p @ v.double().abs()
+    e = 128 * 2.0 ** -23 / np.sqrt(cc.D) * (q.double().abs() @ k.double().abs().T).amax(dim=1, keepdim=True)
+    tiny = p.amax(dim=1, keepdim=True) * 2.0 ** -32 * v.double().abs().sum(0)  # P below 2^-14, 2^7 times the weight
+    # sums: 8192 tiles and parts, a tile's 128, 2^-23 each, of P V and of P
+    bound = 2.0 ** -11 * (a + out.abs()) + 2 * e * a + 2 * (8192 + 128) * 2.0 ** -23 * a + tiny + 2.0 ** -25
+    return out, bound
+
+
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_a_million_positions_by_value(i4lib, cuda, n):
+    """The longest row of the page table, V with a mean, and one position in every 2^16 whose weight is some 3 % of all: a lost
+    part or a zero would be far outside the bound, which the test shows first."""
+    import torch
+    ctx, page = 1 << 20, 128
+    gen = torch.Generator(device=cuda).manual_seed(n)
+    k, v = (torch.randn((ctx // page, 1, page, 128), generator=gen, device=cuda, dtype=torch.float16) for _ in range(2))
+    v += 1
+    perm = torch.randperm(ctx // page, generator=gen, device=cuda)
+    q = torch.randn((n, 4, 128), generator=gen, device=cuda, dtype=torch.float16)
+    q[:, :, 0] = 16
+    for i in range(16):  # a score of 16 * 8.5 / sqrt(128) = 12 beside the other dims', and V far from the mean of all
+        t = i * 65536 + 1000 + 3001 * i
+        k[perm[t // page], 0, t % page, 0] = 8.5
+        v[perm[t // page], 0, t % page] = 2.0 if i % 2 else 30.0
+    table = perm.to(torch.int32)[None].contiguous()
+    start, lens = torch.tensor([0, n], dtype=torch.int32, device=cuda), torch.tensor([ctx], dtype=torch.int32, device=cuda)
+    got = i4lib.paged_gqa_chunk(q, k, v, table, start, lens, max_q=n).double()
+    assert i4lib.device_error() == 0
+    kk, vv = (t[perm][:, 0].reshape(-1, 128) for t in (k, v))
+    for i in sorted({0, n // 2, n - 1}):
+        sees = ctx - n + 1 + i
+        want, bound = longest_row(q[i], kk[:sees], vv[:sees])
+        assert bool((want.abs() > bound).all())  # zeros would show
+        part = torch.arange(sees, device=cuda)
+        for a in (0, 1 << 19, sees - 70000):  # and so would a stretch of 7000 positions with a planted one, left out for all heads
+            a = a // 65536 * 65536 + 1000 + 3001 * (a // 65536) - 3500
+            lost, _ = longest_row(q[i], kk[:sees], vv[:sees], keep=(part < a) | (part >= a + 7000))
+            assert bool(((lost - want).abs() > 2 * bound).any())
+        assert bool(((got[i] - want).abs() <= bound).all())
+
+
+# ------------------------------------------------------------------ repeated calls, early launches off
+
+@pytest.mark.parametrize("lens,hq,hkv,page,window", [
+    ([(1, 514), (1, 77), (1, 1000), (1, 2049)], 28, 4, 16, 0),
+    ([(512, 512)], 28, 4, 16, 0),
+    ([(512, 9000)], 28, 4, 64, 0),
+    ([(1, 4093), (301, 2348), (1, 17), (1, 8191), (777, 777), (64, 5000), (0, 100), (1, 1)], 32, 4, 32, 2000),
+])
+def test_every_call_gives_the_same_bits(i4lib, cuda, lens, hq, hkv, page, window):
+    """Also without the early launches, and with other work on the GPU at the same time."""
+    import torch
+    rng = np.random.default_rng(1)
+    k, v, table = cc.paged(lens, hkv, page, rng)
+    q = rng.standard_normal((int(cc.starts(lens)[-1]), hq, cc.D)).astype(np.float16)
+    args = [dev(a, cuda) for a in (q, k, v, table, cc.starts(lens), np.array([c for _, c in lens], dtype=np.int32))]
+    ws = torch.empty(i4lib.paged_gqa_chunk_ws_bytes(), dtype=torch.uint8, device=cuda)
+    run = lambda: i4lib.paged_gqa_chunk(*args, window=window, ws=ws)  # noqa: E731
+    first = run()
+    assert all(torch.equal(run(), first) for _ in range(20))
+    side, x = torch.cuda.Stream(), torch.randn((4096, 4096), device=cuda)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            x = x @ x * 1e-3
+    assert all(torch.equal(run(), first) for _ in range(20))
+    i4lib.set_option("pdl", 0)
+    try:
+        assert all(torch.equal(run(), first) for _ in range(3))
+    finally:
+        i4lib.set_option("pdl", 1)
+    torch.cuda.synchronize()
+    assert i4lib.device_error() == 0

@@ -326,3 +326,12 @@ def test_pages_that_the_caller_counts_itself(i4lib, cuda):
     assert c.compact() == 3
     for p, b in zip(c.pools, before):
         assert np.array_equal(p[:3].cpu().numpy().view(np.uint16), b)
+
+
+def test_a_life_without_early_launches(i4lib, cuda):
+    i4lib.set_option("pdl", 0)
+    try:
+        test_a_life_of_a_cache(i4lib, cuda, 9)
+        test_captured_operations(i4lib, cuda)
+    finally:
+        i4lib.set_option("pdl", 1)
