@@ -355,13 +355,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ uint64_t uniform(uint64_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// A wait that ends: on the barrier, when another role of the CTA gave up, or after ~2 s.
+// A wait that ends: on the barrier, when another role of the CTA gave up, or after ~8 s: a warp that sums its 32 rows of 2^20
+// positions again (plain_row) holds the other roles up for 3.4e9 cycles.
+constexpr long long kWait = 4 * kWaitCycles;
 __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, unsigned parity, volatile int *stop) {
     if (mbar_test(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_test(bar, parity)) {
         if (*stop) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > kWait) {
             *stop = 1;
             record_error(&g_chunk_error, 1);
             return false;
@@ -394,34 +396,52 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 
 // The softmax sums of one row over the positions [lo, hi) by plain loads, for rows whose tensor-core sum met a NaN or an
 // infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. Returns O, and (m, l) in
-// `ml`: its scores are sums in another order than the tensor cores', so it has a maximum of its own. A lane has the score
-// of one position of 32, then four dims of the sum over them (some 25 cycles a position, so that a row of 2^20 positions
-// stays far inside the other warps' waits).
+// `ml`: its scores are sums in another order than the tensor cores', so it has a maximum of its own. Four lanes have the
+// score of a position, eight positions at a time and 32 a trip; then a lane has four dims of the sum over the 32. Bound by the
+// latency of the loads of a warp that has little beside it: some 100 cycles a position with 16 loads in flight, 285 with one.
 struct PlainRow {
     float4 o;
     float2 ml;
 };
 __device__ __noinline__ PlainRow plain_row(const ChunkAttnParams &p, int b, int g, const uint16_t *q, int lo, int hi, float qs) {
     const int lane = threadIdx.x & 31;
+    uint4 x[4];  // 16-byte chunks lane % 4, + 4, + 8, + 12 of q
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4 *>(q + 8 * (4 * i + (lane & 3)));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
     for (int u0 = lo; u0 < hi; u0 += 32) {
         const int u = u0 + lane;
         const int page = u < hi ? p.page_table[(size_t)b * p.max_pages + u / p.page_size] : -1;
-        const bool there = page >= 0 && page < p.num_pages;  // else K and V are zeros
+        const bool there = page >= 0 && page < p.num_pages;  // else K and V are zeros; the first page's are read and dropped
         const size_t off = there ? (((size_t)page * p.Hkv + g) * p.page_size + u % p.page_size) * 128 : 0;
-        float s = u < hi ? 0.f : -INFINITY;
-        if (there)
-            for (int c = 0; c < 128; c += 8) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(p.k_pool + off + c), x = *reinterpret_cast<const uint4 *>(q + c);
-                s = fma2_f16_f32(a.x, x.x, s);
-                s = fma2_f16_f32(a.y, x.y, s);
-                s = fma2_f16_f32(a.z, x.z, s);
-                s = fma2_f16_f32(a.w, x.w, s);
+        float s = 0.f;
+        uint4 a[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint16_t *k = p.k_pool + __shfl_sync(0xffffffffu, (unsigned long long)off, 8 * c + (lane >> 2)) + 8 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[c][i] = *reinterpret_cast<const uint4 *>(k + 32 * i);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t = fma2_f16_f32(a[c][i].x, x[i].x, t);
+                t = fma2_f16_f32(a[c][i].y, x[i].y, t);
+                t = fma2_f16_f32(a[c][i].z, x[i].z, t);
+                t = fma2_f16_f32(a[c][i].w, x[i].w, t);
             }
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            t = __shfl_sync(0xffffffffu, t, 4 * (lane & 7));
+            if (lane >> 3 == c) s = t;
+        }
+        s = u >= hi ? -INFINITY : (there ? s : 0.f);
         float mx = s;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        for (int e = 16; e > 0; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
         if (mx > m) {
             const float alpha = ex2((m - mx) * qs);
             m = mx;
@@ -431,16 +451,23 @@ __device__ __noinline__ PlainRow plain_row(const ChunkAttnParams &p, int b, int 
         const float w = m == -INFINITY ? 0.f : ex2(fmaf(s - m, qs, kLift));
         l += w;
         const unsigned rows = __ballot_sync(0xffffffffu, there);
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)off, k);
-            if (!((rows >> k) & 1)) continue;
-            const uint2 v = *reinterpret_cast<const uint2 *>(p.v_pool + at + 4 * lane);
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-            const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-            o = make_float4(fmaf(wk, a.x, o.x), fmaf(wk, a.y, o.y), fmaf(wk, c.x, o.z), fmaf(wk, c.y, o.w));
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);  // this trip's sum: a row of 2^20 positions adds 2^15 of them
+#pragma unroll
+        for (int k0 = 0; k0 < 32; k0 += 16) {
+            uint2 v[16];  // in flight together: a warp alone with its loads waits 280 cycles for each
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                v[k] = *reinterpret_cast<const uint2 *>(p.v_pool + __shfl_sync(0xffffffffu, (unsigned long long)off, k0 + k) + 4 * lane);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+                if (!((rows >> (k0 + k)) & 1)) v[k] = make_uint2(0u, 0u);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v[k].x));
+                const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&v[k].y));
+                d = make_float4(fmaf(wk, a.x, d.x), fmaf(wk, a.y, d.y), fmaf(wk, c.x, d.z), fmaf(wk, c.y, d.w));
+            }
         }
+        o = make_float4(o.x + d.x, o.y + d.y, o.z + d.z, o.w + d.w);
     }
     return {o, make_float2(m, warp_sum(l))};
 }

@@ -75,6 +75,36 @@ def test_the_most_tokens(i4lib, cuda):
         assert bool(((got[t, 0].double() - want).abs() <= bound).all()), t
 
 
+def test_rows_summed_again_over_long_contexts(i4lib, cuda):
+    """A NaN in the last token's V makes 15 of 16 tokens be summed again over 2^19 positions, 32 rows a warp, in two whole units a
+    CTA: longer than any other wait of the kernel may take, and the second unit's roles wait for it."""
+    import torch
+    ctx, page, n_seq, n, heads = 1 << 19, 128, 296, 16, 8
+    gen = torch.Generator(device=cuda).manual_seed(7)
+    k, v = (torch.randn((ctx // page, 1, page, 128), generator=gen, device=cuda, dtype=torch.float16) for _ in range(2))
+    v += 1
+    q = torch.randn((n_seq * n, heads, 128), generator=gen, device=cuda, dtype=torch.float16)
+    perm = torch.randperm(ctx // page, generator=gen, device=cuda)
+    v[perm[-1], 0, -1] = float("nan")
+    table = perm.to(torch.int32)[None].repeat(n_seq, 1).contiguous()
+    start = torch.arange(0, n_seq * n + 1, n, dtype=torch.int32, device=cuda)
+    lens = torch.full((n_seq,), ctx, dtype=torch.int32, device=cuda)
+    got = i4lib.paged_gqa_chunk(q, k, v, table, start, lens, max_q=n).view(n_seq, n, heads, 128).double()
+    assert i4lib.device_error() == 0
+    assert bool(torch.isnan(got[:, -1]).all()) and bool(torch.isfinite(got[:, :-1]).all())
+    kk, vv = (t[perm][:, 0].reshape(-1, 128).double() for t in (k, v))
+    for b, i in ((0, 0), (0, 14), (100, 7), (147, 3), (148, 14), (295, 0), (295, 14)):
+        sees = ctx - n + 1 + i
+        s = q[b * n + i].double() @ kk[:sees].T / np.sqrt(128)
+        p = torch.softmax(s, dim=1)
+        want, a = p @ vv[:sees], p @ vv[:sees].abs()
+        e = 128 * 2.0 ** -23 / np.sqrt(128) * (q[b * n + i].double().abs() @ kk[:sees].abs().T).amax(dim=1, keepdim=True)
+        # the result's rounding and exp's approximation, its scores, fp32 sums of 2^14 trips of 32 (of P V and of P)
+        bound = 2.0 ** -11 * want.abs() + 2.0 ** -20 * a + 2 * e * a + 2 * (2 ** 14 + 32) * 2.0 ** -23 * a + 2.0 ** -25
+        assert bool((want.abs() > 8 * bound).all())
+        assert bool(((got[b, i] - want).abs() <= bound).all()), (b, i)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rope_append_with_the_most_heads(i4lib, cuda, interleaved):
     import torch
