@@ -518,12 +518,12 @@ class ChunkedDecoder:
         if P not in (8, 16, 32, 64, 128) or s.head_dim != 128 or s.n_q % s.n_kv or s.n_q // s.n_kv > 8 or row > 1 << 20:
             raise ValueError(f"ChunkedDecoder: pages of {P}, {s.n_q} heads of {s.head_dim} on {s.n_kv} and page-table rows of {row} "
                              "positions are not served (see paged_gqa_chunk)")
-        kv = (cache.num_pages, s.n_kv, P, s.head_dim)
-        if cache.page_size != P or len(cache.k_pools) != s.layers or tuple(cache.k_pools[0].shape) != kv or cache.refs.device != dev:
-            raise ValueError(f"ChunkedDecoder: the cache ({len(cache.k_pools)} layers of {tuple(cache.k_pools[0].shape)} on "
-                             f"{cache.refs.device}) is not one of this model's ({s.layers} of {kv} on {dev})")
         if not 1 <= int(max_tokens) <= 65535:
             raise ValueError(f"ChunkedDecoder: max_tokens {max_tokens} (1 to 65535)")
+        kv, on = (cache.num_pages, s.n_kv, P, s.head_dim), model.glob["embed"].device
+        if cache.page_size != P or len(cache.k_pools) != s.layers or tuple(cache.k_pools[0].shape) != kv or cache.refs.device != on:
+            raise ValueError(f"ChunkedDecoder: the cache ({len(cache.k_pools)} layers of {tuple(cache.k_pools[0].shape)} on "
+                             f"{cache.refs.device}) is not one of this model's ({s.layers} of {kv} on {on})")
         self.model, self.cache, self.shape = model, cache, s
         self.n_max = n = int(max_tokens)
         f16 = dict(dtype=torch.float16, device=dev)

@@ -192,3 +192,12 @@ def test_a_cache_of_another_model_is_refused(i4lib, cuda, model, parts):
         cache = i4lib.PagedCache(i4lib.DeviceModel(other, *weights, device=cuda), n_seqs=2, num_pages=8)
         with pytest.raises(ValueError, match="cache"):
             i4lib.ChunkedDecoder(model, cache, max_tokens=16)
+
+
+@pytest.mark.parametrize("device", ["cuda", "cuda:0"])
+def test_a_model_whose_device_is_a_name(i4lib, cuda, parts, device):
+    model = i4lib.DeviceModel(SHAPE, *parts, device=device)
+    dec = i4lib.ChunkedDecoder(model, i4lib.PagedCache(model, n_seqs=2, num_pages=8), max_tokens=16)
+    text = Text(parts)
+    nxt = text.feed(dec, {1: [3, 1, 4]})
+    text.feed(dec, {0: [1, 5], 1: [nxt[1]]})
