@@ -398,7 +398,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 // infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. Returns O, and (m, l) in
 // `ml`: its scores are sums in another order than the tensor cores', so it has a maximum of its own. Four lanes have the
 // score of a position, eight positions at a time and 32 a trip; then a lane has four dims of the sum over the 32. Bound by the
-// latency of the loads of a warp that has little beside it: some 100 cycles a position with 16 loads in flight, 285 with one.
+// latency of the loads of a warp that has little beside it: some 100 cycles a position with 16 loads of K and 8 of V in flight, 285 with one.
 struct PlainRow {
     float4 o;
     float2 ml;
@@ -453,13 +453,13 @@ __device__ __noinline__ PlainRow plain_row(const ChunkAttnParams &p, int b, int 
         const unsigned rows = __ballot_sync(0xffffffffu, there);
         float4 d = make_float4(0.f, 0.f, 0.f, 0.f);  // this trip's sum: a row of 2^20 positions adds 2^15 of them
 #pragma unroll
-        for (int k0 = 0; k0 < 32; k0 += 16) {
-            uint2 v[16];  // in flight together: a warp alone with its loads waits 280 cycles for each
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+            uint2 v[8];  // in flight together: a warp alone with its loads waits 280 cycles for each
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < 8; ++k)
                 v[k] = *reinterpret_cast<const uint2 *>(p.v_pool + __shfl_sync(0xffffffffu, (unsigned long long)off, k0 + k) + 4 * lane);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
                 if (!((rows >> (k0 + k)) & 1)) v[k] = make_uint2(0u, 0u);
                 const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v[k].x));

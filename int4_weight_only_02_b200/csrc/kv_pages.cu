@@ -479,7 +479,8 @@ struct PlanState {
     cudaError_t err = cudaSuccess;
 };
 
-static int plan_smem(const char *what) {
+static int plan_smem(size_t bytes, const char *what) {
+    if (bytes <= 47 * 1024) return I4_OK;
     static PlanState state[kMaxDevices];
     int dev = 0;
     const int st = cuda_check(cudaGetDevice(&dev), what);
@@ -552,7 +553,7 @@ extern "C" int i4_kv_pages_reserve(const i4_kv_cache *cache, const int32_t *seqs
     if (st || n == 0) return st;
     if (n > cache->n_seqs) return fail(I4_EINVAL, "i4_kv_pages_reserve: %d requests for %d sequences", n, cache->n_seqs);
     const size_t smem = (size_t)cache->n_seqs * sizeof(int);
-    if ((st = plan_smem("i4_kv_pages_reserve"))) return st;
+    if ((st = plan_smem(smem, "i4_kv_pages_reserve"))) return st;
     return cuda_check(launch(kv_reserve_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), seqs,
                              add, n, status, ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs))),
                       "i4_kv_pages_reserve");
@@ -569,7 +570,7 @@ extern "C" int i4_kv_pages_fork(const i4_kv_cache *cache, void *const *pools, in
     size_t smem = ((size_t)cache->n_seqs + cache->num_pages) * sizeof(int);
     const int smem_refs = smem <= kPlanSmem;
     if (!smem_refs) smem = (size_t)cache->n_seqs * sizeof(int);
-    if ((st = plan_smem("i4_kv_pages_fork"))) return st;
+    if ((st = plan_smem(smem, "i4_kv_pages_fork"))) return st;
     const Lists L = ws_lists(ws, ws_cap(cache->num_pages, cache->n_seqs));
     st = cuda_check(launch(kv_fork_kernel, dim3(1), dim3(kPlanThreads), smem, (cudaStream_t)stream, g_pdl, cache_args(cache), src, dst,
                            n, status, L, smem_refs),
