@@ -16,8 +16,9 @@
 //    (m, l, O) in the workspace and a second kernel joins them in order; a unit of at most kWhole tiles is not cut, since
 //    joining costs as much. The lengths are read on the device: every CTA finds its stretch by itself with two block-wide scans.
 //  * Data. One warp loads K and V tiles (32 KB) page by page with TMA into a ring, 128-byte
-//    swizzled (64 single tokens at 8000 positions: 5.6 TB/s with pages of 64, 4.2-4.7 with pages of 16, whose boxes of 2 KB
-//    are bound by the rate at which an SM's TMA takes them); a page outside the pools, or one that no row sees, is an
+//    swizzled (64 single tokens at 8000 positions, 28 heads on 4: 4.6-4.9 TB/s with pages of 64, 4.1-4.3 with pages of 16,
+//    whose boxes of 2 KB are bound by the rate at which an SM's TMA takes them; the single-token kernel of attention.cu, which
+//    gathers pages by cp.async, reads 6.0-6.3 at either); a page outside the pools, or one that no row sees, is an
 //    out-of-range coordinate, which fills zeros.
 //  * Math. S = Q K^T (M = 128 rows, both operands K-major in shared memory) into tensor memory; the 128 threads of a
 //    warpgroup own one row each, so maximum and sum need no exchange; P = 2^(S - m + 7), rounded to fp16 (the tensor cores'
@@ -38,11 +39,13 @@
 //    waiting for its own product.
 //
 // Bound by the tensor cores and their power: S of 64 positions is fed at the A operand's rate, so a tile of 2 x 128 rows
-// costs 48 products of 64 cycles, 93 % of the 3300 cycles measured, and under a steady load the GPU's power limit holds the
-// clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 211 us in short runs, 1130 TFLOP/s, 247 us under a
-// steady load, 967 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 425 and 494 us. Few rows are bound by the chain of dependent
+// costs 48 products of 64 cycles, 93 % of the 3300 cycles measured (32 products of twice the width would do the same work), and
+// under a steady load the GPU's power limit holds the
+// clock near 1.6 GHz. 512 tokens behind 32768 positions (28 heads on 4): 212-219 us in short runs, 1090-1130 TFLOP/s, 245-252 us
+// under a steady load, 950-975 TFLOP/s (cuBLAS: 1421); a prompt of 8192: 437 and 498 us. Few rows are bound by the chain of dependent
 // steps: four single tokens at up to 2049 positions take 14 us, 3.5 to the first tile (lengths, scans, first loads), 2 a
-// tile, 1.2 to store a part and 3.5 to join them; a prompt of 512 takes 17 us.
+// tile, 1.2 to store a part and 3.5 to join them (attention.cu's kernel, whose parts meet inside a cluster, takes 8.8); a prompt
+// of 512 takes 17 us where the page-table row ends at 1024 positions, else 19.5.
 #include <cmath>
 
 #include "chunk.cuh"
@@ -1163,7 +1166,8 @@ extern "C" int i4_paged_gqa_chunk(const i4_chunk_attn_args *args, void *stream) 
     p.part_o = reinterpret_cast<float *>(w + kWsO);
     p.slot_tokens = kRows / G;
     // One slot of 128 rows when every chunk fits it: the other warpgroup would idle. Also when units of one slot find an SM each
-    // and have a few tiles only: a slot alone takes a tile in 1.3 us, two in 1.9, and the kernel begins and ends sooner. (28
+    // and have a few tiles only, as far as the host can tell from the width of the page table and the number of its rows (a cache
+    // of wide rows or many slots does not get there: the prompt of 512 below then takes 19.5 us): a slot alone takes a tile in 1.3 us, two in 1.9, and the kernel begins and ends sooner. (28
     // heads on 4, 512 tokens at 512 positions: 17.0 us against 19.6, at 1024: 26.5 and 26.0, at 2048: 38.4 against 32.5; 256
     // tokens: 13.4 against 16.0, 21.4 against 23.0, 27.7 against 25.7.)
     const int longest = max_q > 0 && max_q < T ? max_q : T;

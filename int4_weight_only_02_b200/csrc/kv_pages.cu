@@ -11,9 +11,11 @@
 // over them: several CTAs would need grid-wide barriers that cost as much) and
 // leave a list of copies in the workspace; a second kernel over the whole GPU,
 // brought up while the first runs, moves the data of all pools at once and is
-// bound by HBM. Three forks of a short sequence in 4 pools take 7.6 us, 63 of
-// one of 4015 tokens in 56 pools 22 us (12 to decide; 54 MB written), compacting
-// 9 pages of 4 pools 7 us, 300 pages of 56 pools 95 us (551 MB, 5.8 TB/s).
+// bound by HBM. Three forks of a short sequence in 4 pools take 7.4 us, 63 of
+// one of 4015 tokens in 56 pools 21.5 us (12 to decide; 54 MB written, the one
+// source page read once from HBM), compacting 9 pages of 4 pools 7 us, 300 pages
+// of 56 pools 95 us (12 to decide). Reserving 17 tokens for each of 64 sequences
+// and freeing them again takes 9.9 us, for 512 sequences in 65536 pages 23.
 #include <mutex>
 
 #include "chunk.cuh"
@@ -358,7 +360,8 @@ __device__ __forceinline__ void copy_span(unsigned char *dst, const unsigned cha
 
 // Whole pages src[i] -> dst[i] of pool blockIdx.y; n_dev, when given, is the device's count. Work item: (i, part of the page). The
 // first remap_blocks blocks of a row of the grid instead give table entries of held pages at or above n_live (n_dev[1])
-// the page's new id. Bound by HBM: 300 pages of 56 pools (551 MB) in 83 us, 6.6 TB/s.
+// the page's new id. Bound by HBM: 300 pages of 56 pools in 83 us, of whose 551 MB 501 have passed HBM by then (6.0 TB/s); the
+// rest is written back from L2 later.
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ PoolPtrs pools, const int32_t *src,
                                                                const int32_t *dst, int n, const int32_t *n_dev, int num_pages,
                                                                int page_vecs, int parts, const CacheArgs c, const int32_t *new_id,
