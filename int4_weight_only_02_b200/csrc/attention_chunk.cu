@@ -359,7 +359,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 __device__ __forceinline__ uint64_t uniform(uint64_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A wait that ends: on the barrier, when another role of the CTA gave up, or after ~8 s: a warp that sums its 32 rows of 2^20
-// positions again (plain_row) holds the other roles up for 3.4e9 cycles.
+// positions again (plain_row) holds the other roles up for 3.4e9 cycles, 4.6e9 where both slots do.
 constexpr long long kWait = 4 * kWaitCycles;
 __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, unsigned parity, volatile int *stop) {
     if (mbar_test(bar, parity)) return true;
@@ -401,7 +401,8 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
 // infinity: P = 0 times such a value of a position that other rows see is NaN, and must not count. Returns O, and (m, l) in
 // `ml`: its scores are sums in another order than the tensor cores', so it has a maximum of its own. Four lanes have the
 // score of a position, eight positions at a time and 32 a trip; then a lane has four dims of the sum over the 32. Bound by the
-// latency of the loads of a warp that has little beside it: some 100 cycles a position with 16 loads of K and 8 of V in flight, 285 with one.
+// latency of the loads of a warp that has little beside it: some 100 cycles a position with 16 loads of K and 8 of V in flight
+// (137 with two slots a CTA), 285 with one.
 struct PlainRow {
     float4 o;
     float2 ml;
